@@ -15,6 +15,14 @@
  *                          bonus token, accepted lengths and emitted tokens
  *                          (dspark_verify_target_stats / dspark_verify_from_stats:
  *                          its two halves, so the first can run beside the draft)
+ * and of the logit head in front of a round and the token scores behind it:
+ *   dspark_residual_norm   residual addition and root-mean-square norm, to the
+ *                          input's type or e4m3 with a scale per row; its gradient
+ *   dspark_linear          product with a weight matrix (hidden states to logits),
+ *                          scales, bias, activation and residual in its epilogue;
+ *                          its gradient
+ *   dspark_token_logprobs  log probabilities of given tokens, entropy and the most
+ *                          likely alternatives of every row; its gradient
  *
  * Sources, cited by page title and section:
  *   [P1] "DSpark turns speculation into a scheduler" (benebsworth.pages.dev)
@@ -59,7 +67,8 @@ extern "C" {
 /* Same underlying type as cudaStream_t, so that C callers need no CUDA header. */
 typedef struct CUstream_st* dspark_stream_t;
 
-enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 };
+/* DSPARK_E4M3 (8 bits, 4 exponent, 3 mantissa, no infinity) only where a call names it. */
+enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2 };
 
 enum {
   DSPARK_OK = 0,
@@ -70,7 +79,19 @@ enum {
   DSPARK_ERR_TIMEOUT = -5       /* reported by dspark_read_status only       */
 };
 
-enum { DSPARK_OP_DRAFT = 0, DSPARK_OP_SCHEDULE = 1, DSPARK_OP_VERIFY = 2, DSPARK_OP_CALIB = 3 };
+enum {
+  DSPARK_OP_DRAFT = 0,
+  DSPARK_OP_SCHEDULE = 1,
+  DSPARK_OP_VERIFY = 2,
+  DSPARK_OP_CALIB = 3,
+  DSPARK_OP_LOGPROBS = 4,
+  DSPARK_OP_NORM = 5,
+  DSPARK_OP_LINEAR = 6
+};
+
+/* Activations of dspark_linear. GELU is the tanh form,
+ * z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))). */
+enum { DSPARK_ACT_NONE = 0, DSPARK_ACT_RELU = 1, DSPARK_ACT_SILU = 2, DSPARK_ACT_GELU = 3 };
 
 /* Prefix-cut modes of dspark_prefix_schedule. */
 enum { DSPARK_CUT_COST = 0, DSPARK_CUT_THRESHOLD = 1, DSPARK_CUT_NONE = 2 };
@@ -85,8 +106,12 @@ enum { DSPARK_CUT_COST = 0, DSPARK_CUT_THRESHOLD = 1, DSPARK_CUT_NONE = 2 };
 
 /*
  * Workspace bytes needed by operation `op` (DSPARK_OP_*) for these sizes
- * (r is ignored except by DSPARK_OP_DRAFT). Pure host function. Returns 0 for
- * unsupported arguments. One workspace of the largest size may serve all the
+ * (r is read by DSPARK_OP_DRAFT and DSPARK_OP_LINEAR only). Pure host function. Returns 0 for
+ * unsupported arguments. The last three operations, whose sizes carry other
+ * names, take: LOGPROBS B, K = rows per request (J), V, dtype; NORM B = rows (M),
+ * V = width (H); LINEAR B = rows (M), V = outputs (N), r = inputs (K), dtype =
+ * the operands' type (BF16 or E4M3). What an operation does not name is ignored.
+ * One workspace of the largest size may serve all the
  * operations of a round: the draft's chunk partials and verification's target
  * statistics occupy different regions of it, so dspark_verify_target_stats may
  * run beside dspark_draft_sample; otherwise the calls must not overlap.
@@ -366,6 +391,133 @@ int dspark_sts_fit(const float* conf_logit, const uint8_t* survived, int N, int 
                    float* T_out, int32_t* index_out, float* ece_before,
                    float* ece_after, void* ws, size_t ws_bytes,
                    dspark_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the most likely
+ * alternatives of their rows: what a server returns beside the tokens a round
+ * emitted, and the loss terms of a policy or of a drafter trained on them.
+ *
+ * For every request b and row j < J with token v = tok[b,j], x = logits[b,j] / temp[b]:
+ *   lse = ln sum_i exp(x_i),  logp = x_v - lse,
+ *   entropy = -sum_i p_i ln p_i with p = softmax(x),
+ *   top_idx[b,j,:] = the n_top entries of largest logit, descending (lowest index
+ *   first on ties), top_logp their x - lse.
+ * Masked entries (-inf) have p = 0, log probability -inf, and come last among
+ * the alternatives, by index.
+ * A request of temperature 0 (greedy) is scored at temperature 1.
+ * tok[b,j] = -1 marks padding (dspark_verify's out behind the emitted tokens
+ * can be passed as it is): nothing of the row is read, and logp = entropy = lse
+ * = 0, top_idx = -1, top_logp = -inf. Rows in error (a token outside [-1, V),
+ * NaN, +inf or nothing but -inf among the logits, a negative or NaN
+ * temperature) get the same values and set their status bit.
+ *
+ *   logits [B, J, V] dtype, tok [B, J] i32, temp [B] f32 or NULL (1)
+ *   logp [B, J] f32 out; entropy, lse [B, J] f32 out or NULL
+ *   top_idx [B, J, n_top] i32 out, top_logp [B, J, n_top] f32 out (NULL with n_top 0)
+ * Limits: 1 <= B <= 65535, 1 <= J <= 64, 8 <= V < 2^24, V % 8 == 0,
+ * 0 <= n_top <= min(32, V). Each row is read once; sums are fp32.
+ * Workspace: dspark_workspace_bytes(DSPARK_OP_LOGPROBS, B, J, V, 0, dtype) (the
+ * status block alone). One launch.
+ */
+int dspark_token_logprobs(const void* logits, const int32_t* tok, const float* temp, int B, int J,
+                          int V, int dtype, int n_top, float* logp, float* entropy, float* lse,
+                          int32_t* top_idx, float* top_logp, void* ws, size_t ws_bytes,
+                          dspark_stream_t stream);
+
+/*
+ * Gradient of sum g_logp logp + g_entropy entropy with respect to the logits:
+ *   dlogits_i = (1 / temp) [ g_logp (1[i = v] - p_i) - g_entropy p_i (ln p_i + entropy) ]
+ * rounded once to dtype. lse and entropy are dspark_token_logprobs' outputs for
+ * the same logits and temperatures (entropy is read only with g_entropy). Padded
+ * rows, and rows in error (as above; here a row whose lse is not finite counts
+ * as one, the logits are not looked at), get zeros. dlogits may be logits.
+ *
+ *   logits [B, J, V] dtype, tok [B, J] i32, temp [B] f32 or NULL
+ *   lse, g_logp [B, J] f32; entropy, g_entropy [B, J] f32 or both NULL
+ *   dlogits [B, J, V] dtype out
+ * Limits and workspace as for dspark_token_logprobs. One launch.
+ */
+int dspark_token_logprobs_grad(const void* logits, const int32_t* tok, const float* temp,
+                               const float* lse, const float* entropy, const float* g_logp,
+                               const float* g_entropy, int B, int J, int V, int dtype,
+                               void* dlogits, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Residual addition and root-mean-square norm of M rows of width H:
+ *   v = x + delta (fp32),  rstd = (sum_h v_h^2 / H + eps)^(-1/2),  y = v rstd weight
+ * sum = v rounded to dtype (the residual stream handed on), y rounded once from
+ * the fp32 v to y_type: dtype, or DSPARK_E4M3 with one scale per row,
+ *   y_scale = max(max_h |y_h| / 448, 2^-126),  y8 = e4m3(y / y_scale).
+ * A row whose sum of squares is not finite in fp32 (NaN, infinity, or entries
+ * past 1e19) becomes NaN (y, rstd, y_scale) and sets DSPARK_STATUS_BAD_ROW with
+ * the row's index as the request.
+ *
+ *   x, weight [M, H], [H] dtype; delta [M, H] dtype or NULL (no addition)
+ *   sum [M, H] dtype out or NULL; it may be x or delta
+ *   y [M, H] y_type out (no other tensor's memory); y_scale [M] f32 out (DSPARK_E4M3), rstd [M] f32 out or NULL
+ * Limits: M >= 1, 8 <= H <= 16384, H % 8 == 0, eps >= 0.
+ * Workspace: dspark_workspace_bytes(DSPARK_OP_NORM, M, 0, H, 0, 0). One launch.
+ */
+int dspark_residual_norm(const void* x, const void* delta, const void* weight, int M, int H,
+                         int dtype, float eps, void* sum, void* y, int y_type, float* y_scale,
+                         float* rstd, void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Gradient of dspark_residual_norm (y in dtype). With s the stored sum, rstd its
+ * output, dy the gradient of y and dsum the gradient that reaches the sum
+ * directly (NULL: none):
+ *   dx = dsum + rstd (weight dy - s rstd^2 mean_h(weight dy s))
+ *   dweight = sum over rows of dy s rstd
+ * dx is the gradient of x and of delta alike. dweight (fp32) is summed in a
+ * fixed order. dx may be dy or dsum.
+ *
+ *   s, dy [M, H], weight [H], dsum [M, H] or NULL dtype; rstd [M] f32
+ *   dx [M, H] dtype out; dweight [H] f32 out or NULL
+ * Limits and workspace as for dspark_residual_norm. One launch, two with dweight.
+ */
+int dspark_residual_norm_grad(const void* s, const void* weight, const float* rstd, const void* dy,
+                              const void* dsum, int M, int H, int dtype, void* dx, float* dweight,
+                              void* ws, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Product of M rows of K entries with a weight matrix of N rows (as a linear
+ * layer stores it), everything that follows fused into its epilogue:
+ *   pre = x_scale[m] w_scale[n] sum_k x[m,k] w[n,k] + bias[n]
+ *   y = act(pre) + residual[m,n]
+ * on the tensor cores with fp32 accumulation; y and pre are rounded once. With
+ * the e4m3 output and scales of dspark_residual_norm as x, in_type DSPARK_E4M3
+ * multiplies 8-bit operands.
+ *
+ *   x [M, K], w [N, K] in_type (DSPARK_BF16 or DSPARK_E4M3)
+ *   x_scale [M], w_scale [N] f32 (both with DSPARK_E4M3, both NULL with DSPARK_BF16)
+ *   bias [N] f32 or NULL; residual [M, N] out_type or NULL (it may be y)
+ *   y [M, N] out_type (DSPARK_F32 or DSPARK_BF16) out; pre [M, N] out_type out or NULL (for the gradient)
+ *   act DSPARK_ACT_*
+ * Limits: 1 <= M, N < 2^24, 1 <= K < 2^20, K a multiple of 16 bytes (8 bf16, 16
+ * e4m3 entries); x and w 16-byte aligned, y, pre and residual aligned to their
+ * type. Small outputs split K over SMs; the parts are added in a fixed order.
+ * Workspace: dspark_workspace_bytes(DSPARK_OP_LINEAR, M, 0, N, K, in_type).
+ */
+int dspark_linear(const void* x, const void* w, const float* x_scale, const float* w_scale,
+                  const float* bias, const void* residual, int M, int N, int K, int in_type,
+                  int out_type, int act, void* y, void* pre, void* ws, size_t ws_bytes,
+                  dspark_stream_t stream);
+
+/*
+ * Gradient of dspark_linear for bf16 operands: with dpre = dy act'(pre),
+ *   dx = dpre w,  dw = dpre^T x,  dbias = sum over rows of dpre
+ * (the residual's gradient is dy itself). dpre is rounded to bf16 for the two
+ * products (their operand type) and enters dbias unrounded. act'(0) of RELU is 0.
+ *
+ *   x [M, K] (with dw), w [N, K] (with dx), dy [M, N], pre [M, N] (act other than NONE) bf16
+ *   dx [M, K] bf16, dw [N, K] bf16, dbias [N] f32 out, each NULL to leave it out
+ * Limits: those of dspark_linear, and N % 8 == 0; every tensor 16-byte aligned.
+ * Outputs must not overlap the inputs.
+ * Workspace as for dspark_linear with DSPARK_BF16.
+ */
+int dspark_linear_grad(const void* x, const void* w, const void* dy, const void* pre, int M, int N,
+                       int K, int act, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                       dspark_stream_t stream);
 
 /*
  * dspark_draft_sample for callers that cannot allocate device memory. The pages

@@ -17,8 +17,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 OP_DRAFT, OP_SCHEDULE, OP_VERIFY, OP_CALIB = 0, 1, 2, 3
+OP_LOGPROBS, OP_NORM, OP_LINEAR = 4, 5, 6
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # gelu: the tanh form
 CUT_COST, CUT_THRESHOLD, CUT_NONE = 0, 1, 2
 STATUS_BAD_TOKEN, STATUS_BAD_ROW, STATUS_BAD_CUT, STATUS_BAD_TEMP, STATUS_TIMEOUT = 1, 2, 4, 8, 16
 STATUS_INTERNAL = 32
@@ -52,6 +54,14 @@ SIGNATURES = {
     "dspark_draft_sample_static": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _u64, _u64,
                                         _p, _p, _p, _p, _p, _p]),
     "dspark_sts_fit": (_i, [_p, _p, _i, _i, _p, _p, _p, _p, _p, _sz, _p]),
+    "dspark_token_logprobs": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _sz,
+                                   _p]),
+    "dspark_token_logprobs_grad": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _sz,
+                                        _p]),
+    "dspark_residual_norm": (_i, [_p, _p, _p, _i, _i, _i, _f, _p, _p, _i, _p, _p, _p, _sz, _p]),
+    "dspark_residual_norm_grad": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _sz, _p]),
+    "dspark_linear": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p, _sz, _p]),
+    "dspark_linear_grad": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
     "dspark_read_status": (_i, [_p, _p, ctypes.POINTER(ctypes.c_uint32),
                                 ctypes.POINTER(ctypes.c_int32)]),
     "dspark_clear_status": (_i, [_p, _p]),
@@ -342,6 +352,127 @@ def sts_fit(conf_logit, survived, T_out, index_out, ece_before, ece_after, ws, s
         _ptr(ece_before, "ece_before", f32, (K,), dev), _ptr(ece_after, "ece_after", f32, (K,), dev),
         _ptr(ws, "ws", None, None, dev), ws.numel() * ws.element_size())
     _call("dspark_sts_fit", dev, args, stream)
+
+
+def token_logprobs(logits, tok, temp, logp, ws, entropy=None, lse=None, top_idx=None,
+                   top_logp=None, stream=None) -> None:
+    """dspark_token_logprobs: logits [B,J,V], tok [B,J] (-1 = padding), temp [B] or None ->
+    logp [B,J], and where given entropy, lse [B,J], top_idx, top_logp [B,J,n]."""
+    B, J, V = logits.shape
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    if (top_idx is None) != (top_logp is None):
+        raise DSparkError("top_idx and top_logp go together")
+    n = 0
+    if top_idx is not None:
+        if top_idx.dim() != 3:
+            raise DSparkError(f"top_idx must have shape {(B, J)} + (n,), got {tuple(top_idx.shape)}")
+        n = top_idx.shape[2]
+    args = (
+        _ptr(logits, "logits", None, (B, J, V), dev), _ptr(tok, "tok", i32, (B, J), dev),
+        _ptr(temp, "temp", f32, (B,), dev), B, J, V, _dtype_code(logits), n,
+        _ptr(logp, "logp", f32, (B, J), dev), _ptr(entropy, "entropy", f32, (B, J), dev),
+        _ptr(lse, "lse", f32, (B, J), dev), _ptr(top_idx, "top_idx", i32, (B, J, n), dev),
+        _ptr(top_logp, "top_logp", f32, (B, J, n), dev), _ptr(ws, "ws", None, None, dev),
+        ws.numel() * ws.element_size())
+    _call("dspark_token_logprobs", dev, args, stream)
+
+
+def token_logprobs_grad(logits, tok, temp, lse, g_logp, dlogits, ws, entropy=None, g_entropy=None,
+                        stream=None) -> None:
+    """dspark_token_logprobs_grad: the gradient of sum g_logp logp + g_entropy entropy
+    (entropy and g_entropy go together) with respect to the logits -> dlogits
+    (which may be logits)."""
+    B, J, V = logits.shape
+    dev, f32 = logits.device, torch.float32
+    if (entropy is None) != (g_entropy is None):
+        raise DSparkError("entropy and g_entropy go together")
+    args = (
+        _ptr(logits, "logits", None, (B, J, V), dev), _ptr(tok, "tok", torch.int32, (B, J), dev),
+        _ptr(temp, "temp", f32, (B,), dev), _ptr(lse, "lse", f32, (B, J), dev),
+        _ptr(entropy, "entropy", f32, (B, J), dev), _ptr(g_logp, "g_logp", f32, (B, J), dev),
+        _ptr(g_entropy, "g_entropy", f32, (B, J), dev), B, J, V, _dtype_code(logits),
+        _ptr(dlogits, "dlogits", logits.dtype, (B, J, V), dev), _ptr(ws, "ws", None, None, dev),
+        ws.numel() * ws.element_size())
+    _call("dspark_token_logprobs_grad", dev, args, stream)
+
+
+def residual_norm(x, delta, weight, eps: float, y, ws, sum=None, y_scale=None, rstd=None,
+                  stream=None) -> None:
+    """dspark_residual_norm: x [M,H], delta [M,H] or None, weight [H] -> y [M,H] (x's dtype, or
+    float8_e4m3fn with y_scale [M]), and where given sum [M,H] (x + delta; it may be x or
+    delta) and rstd [M]."""
+    M, H = x.shape
+    dev, f32 = x.device, torch.float32
+    e4m3 = y.dtype == torch.float8_e4m3fn
+    if e4m3 != (y_scale is not None):
+        raise DSparkError("y_scale goes with a float8_e4m3fn y")
+    args = (
+        _ptr(x, "x", None, (M, H), dev), _ptr(delta, "delta", x.dtype, (M, H), dev),
+        _ptr(weight, "weight", x.dtype, (H,), dev), M, H, _dtype_code(x), float(eps),
+        _ptr(sum, "sum", x.dtype, (M, H), dev),
+        _ptr(y, "y", y.dtype if e4m3 else x.dtype, (M, H), dev), E4M3 if e4m3 else _dtype_code(x),
+        _ptr(y_scale, "y_scale", f32, (M,), dev), _ptr(rstd, "rstd", f32, (M,), dev),
+        _ptr(ws, "ws", None, None, dev), ws.numel() * ws.element_size())
+    _call("dspark_residual_norm", dev, args, stream)
+
+
+def residual_norm_grad(s, weight, rstd, dy, dx, ws, dsum=None, dweight=None, stream=None) -> None:
+    """dspark_residual_norm_grad: s [M,H] (the stored sum), rstd [M], dy [M,H], dsum [M,H] or None
+    -> dx [M,H] (which may be dy or dsum), and where given dweight [H] f32."""
+    M, H = s.shape
+    dev, f32 = s.device, torch.float32
+    args = (
+        _ptr(s, "s", None, (M, H), dev), _ptr(weight, "weight", s.dtype, (H,), dev),
+        _ptr(rstd, "rstd", f32, (M,), dev), _ptr(dy, "dy", s.dtype, (M, H), dev),
+        _ptr(dsum, "dsum", s.dtype, (M, H), dev), M, H, _dtype_code(s),
+        _ptr(dx, "dx", s.dtype, (M, H), dev), _ptr(dweight, "dweight", f32, (H,), dev),
+        _ptr(ws, "ws", None, None, dev), ws.numel() * ws.element_size())
+    _call("dspark_residual_norm_grad", dev, args, stream)
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise DSparkError(f"unknown activation {act!r}, one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def linear(x, w, y, ws, x_scale=None, w_scale=None, bias=None, residual=None, pre=None,
+           act: str = "none", stream=None) -> None:
+    """dspark_linear: y [M,N] = act(x_scale w_scale x w^T + bias) + residual for x [M,K] and
+    w [N,K], both bfloat16 or both float8_e4m3fn (then with x_scale [M] and w_scale [N]); y
+    (float32 or bfloat16), residual (which may be y) and pre share a dtype."""
+    M, K = x.shape
+    N = w.shape[0]
+    dev, f32 = x.device, torch.float32
+    e4m3 = x.dtype == torch.float8_e4m3fn
+    if not e4m3 and x.dtype != torch.bfloat16:
+        raise DSparkError(f"x must be bfloat16 or float8_e4m3fn, got {x.dtype}")
+    if e4m3 != (x_scale is not None) or e4m3 != (w_scale is not None):
+        raise DSparkError("x_scale and w_scale go with float8_e4m3fn operands")
+    args = (
+        _ptr(x, "x", None, (M, K), dev), _ptr(w, "w", x.dtype, (N, K), dev),
+        _ptr(x_scale, "x_scale", f32, (M,), dev), _ptr(w_scale, "w_scale", f32, (N,), dev),
+        _ptr(bias, "bias", f32, (N,), dev), _ptr(residual, "residual", y.dtype, (M, N), dev),
+        M, N, K, E4M3 if e4m3 else BF16, _dtype_code(y), _activation(act),
+        _ptr(y, "y", None, (M, N), dev), _ptr(pre, "pre", y.dtype, (M, N), dev),
+        _ptr(ws, "ws", None, None, dev), ws.numel() * ws.element_size())
+    _call("dspark_linear", dev, args, stream)
+
+
+def linear_grad(x, w, dy, ws, dx=None, dw=None, dbias=None, pre=None, act: str = "none",
+                stream=None) -> None:
+    """dspark_linear_grad (bfloat16): dy [M,N] and, with an activation, pre [M,N] -> where given
+    dx [M,K], dw [N,K] and dbias [N] f32."""
+    M, K = x.shape
+    N = w.shape[0]
+    dev, bf16 = x.device, torch.bfloat16
+    args = (
+        _ptr(x, "x", bf16, (M, K), dev), _ptr(w, "w", bf16, (N, K), dev),
+        _ptr(dy, "dy", bf16, (M, N), dev), _ptr(pre, "pre", bf16, (M, N), dev), M, N, K,
+        _activation(act), _ptr(dx, "dx", bf16, (M, K), dev), _ptr(dw, "dw", bf16, (N, K), dev),
+        _ptr(dbias, "dbias", torch.float32, (N,), dev), _ptr(ws, "ws", None, None, dev),
+        ws.numel() * ws.element_size())
+    _call("dspark_linear_grad", dev, args, stream)
 
 
 def selftest_waits(result, ws, stream=None) -> None:

@@ -7,6 +7,9 @@
 #include "common.cuh"
 #include "draft.cuh"
 #include "draft_tc.cuh"
+#include "host.cuh"
+#include "linear.cuh"
+#include "norm.cuh"
 #include "schedule.cuh"
 #include "verify.cuh"
 
@@ -19,11 +22,7 @@ using namespace dspark;
 
 namespace {
 
-constexpr int kAbiVersion = (3 << 16) | 2;
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+constexpr int kAbiVersion = (3 << 16) | 3;
 
 inline int nchunks(int V) { return (V + kChunk - 1) / kChunk; }
 
@@ -42,29 +41,6 @@ inline size_t counter_offset(int B, int K, int V, int dtype) {
   return stats_offset(B, V) + stats_region(B, K, V, dtype);
 }
 inline size_t order_offset(int B, int K, int V, int dtype) { return counter_offset(B, K, V, dtype) + 256; }
-
-bool shape_ok(int B, int K, int V, int dtype) {
-  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return false;
-  if (B < 1 || B > 65535 || K < 1 || K > 64) return false;
-  if (V < 8 || V >= (1 << 24) || V % 8 != 0) return false;
-  return true;
-}
-
-// The fatbin carries sm_100a code only.
-int device_check(int* num_sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
-  if (major != 10 || minor != 0) return DSPARK_ERR_UNSUPPORTED;
-  if (num_sms) *num_sms = sms;
-  return DSPARK_OK;
-}
-
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA; }
 
 }  // namespace
 
@@ -106,6 +82,15 @@ size_t dspark_workspace_bytes(int op, int B, int K, int V, int r, int dtype) {
     case DSPARK_OP_VERIFY:
       if (!shape_ok(B, K, V, dtype)) return 0;
       return order_offset(B, K, V, dtype) + round_up((size_t)B * sizeof(int32_t), 256);
+    case DSPARK_OP_LOGPROBS:
+      if (!shape_ok(B, K, V, dtype)) return 0;
+      return kStatusBytes;
+    case DSPARK_OP_NORM:
+      if (!norm_shape_ok(B, V)) return 0;
+      return kStatusBytes + (size_t)kNormGradBlocks * V * sizeof(float);
+    case DSPARK_OP_LINEAR:
+      if (!linear_shape_ok(B, V, r, dtype)) return 0;
+      return kStatusBytes + linear_scratch_bytes(B, V, r, dtype);
     default:
       return 0;
   }

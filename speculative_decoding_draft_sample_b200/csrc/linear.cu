@@ -1,0 +1,529 @@
+// Linear product with scales, bias, activation and residual in its epilogue, and
+// its gradient, on the tensor cores (tcgen05, operands by TMA).
+//
+//   y[m, n] = act(x_scale[m] w_scale[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+//   dpre = dy act'(pre), dx = dpre w, dw = dpre^T x, dbias = column sums of dpre
+//
+// Orientation: the matrix instruction's 128 rows (tensor-memory lanes) are the
+// output's contiguous index (features), its columns the other one (tokens).
+// One kernel then serves one token and thousands: the column tile is 16 to 256
+// wide, a small batch streams the weights past a few columns, and a warp's
+// store of one column is 32 neighbouring outputs, so the epilogue needs no
+// staging and no alignment of the output's width. The three products differ
+// only in which operand lies contraction-major:
+//   y  [m, n]: lanes n, A = w (k contiguous),  columns m, B = x    (k contiguous)
+//   dx [m, k]: lanes k, A = w (k = lanes contiguous), columns m, B = dpre (n contiguous)
+//   dw [n, k]: lanes k, A = x (k = lanes contiguous), columns n, B = dpre (n = columns contiguous)
+//
+// Persistent CTAs take work units (output tile, part of the contraction):
+//   warp 0     TMA producer: 128-byte-wide boxes of A and B into a ring of stages
+//   warp 1     tensor-memory allocation and the single-thread tcgen05.mma issuer
+//   warps 2-9  epilogue of the previous unit meanwhile (two accumulators): a warp
+//              reads its quarter of the lanes (hardware: warp index mod 4), the two
+//              halves take alternate blocks of 16 columns
+// With fewer tiles than SMs the contraction is split: each part leaves its fp32
+// sums in the workspace and the last to arrive adds them in order of the parts
+// (the result does not depend on who that is) and finishes the tile.
+// Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
+#include "host.cuh"
+#include "linear.cuh"
+#include "norm.cuh"
+#include "tcgen05.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace t5;
+
+constexpr int kThreads = 320;
+constexpr int kEpiThreads = 256;
+constexpr int kTileF = 128;                    // lanes: output features per tile
+constexpr int kMaxCols = 256;                  // columns per tile at most
+constexpr int kABytes = kTileF * 128;          // A of a stage: 128 bytes of contraction (or lanes) x 128
+constexpr int kMaxStages = 12;
+constexpr int kRing = 221184;                  // bytes of the stage ring (216 KB)
+constexpr int kBoxBytes = 64 * 128;            // one [64 x 128 bytes] box of a lane- or column-contiguous operand
+constexpr int kOffBar = kRing;
+constexpr int kNumBars = 2 * kMaxStages + 4;
+constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
+static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory per block");
+constexpr int kPlanSms = 148;                  // SMs that the split of the work is planned for
+
+enum : unsigned int {  // wait sites recorded when a bounded wait gives up
+  kWhereEmpty = 40,
+  kWhereFull = 41,
+  kWhereAccFull = 42,
+  kWhereAccEmpty = 43,
+};
+
+struct Gemm {
+  int F, T;                 // lanes (contiguous outputs) and columns in all
+  int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
+  int nt;                   // columns per tile, a multiple of 16 (64 when B is column-contiguous)
+  int tiles_f, tiles_t, splits;
+  const float* col_scale;   // [T] or null
+  const float* lane_scale;  // [F] or null
+  const float* bias;        // [F] or null
+  const void* residual;     // [T, F] or null
+  void* out;                // [T, F]
+  void* pre;                // [T, F] or null
+  int out_type, act;
+  float* partial;           // [tile, split, nt, 128] (splits > 1)
+  unsigned int* counter;    // [tile], zero at launch (splits > 1)
+  Status* status;
+};
+
+// z / (1 + exp(-v)): silu with v = z, gelu's tanh form with v = 2 sqrt(2/pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gate(float z, float v) { return __fdividef(z, 1.f + ex2(-v * kLog2e)); }
+
+constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case DSPARK_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
+    case DSPARK_ACT_SILU: return gate(z, z);
+    case DSPARK_ACT_GELU: return gate(z, kGelu2 * fmaf(0.044715f * z * z, z, z));
+    default: return z;
+  }
+}
+
+// act'(z); past |z| = 64 both gates are 0 or 1 exactly
+__device__ __forceinline__ float activate_grad(float z, int act) {
+  if (act == DSPARK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  z = z != z ? z : fminf(fmaxf(z, -64.f), 64.f);
+  const float v = act == DSPARK_ACT_SILU ? z : kGelu2 * fmaf(0.044715f * z * z, z, z);
+  const float dv = act == DSPARK_ACT_SILU ? 1.f : kGelu2 * fmaf(3.f * 0.044715f * z, z, 1.f);
+  const float g = __fdividef(1.f, 1.f + ex2(-v * kLog2e));
+  return g + z * g * (1.f - g) * dv;
+}
+
+__device__ __forceinline__ float load_out(const void* p, long long i, int type) {
+  return type == DSPARK_F32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(void* p, long long i, int type, float v) {
+  if (type == DSPARK_F32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<uint16_t*>(p)[i] = Elem<DSPARK_BF16>::store_round(v);
+}
+
+// 16 columns of one lane: scales, bias, activation, residual, rounding, stores.
+__device__ __forceinline__ void finish16(const Gemm& g, const float* acc, int f, int t0) {
+  if (f >= g.F) return;
+  const float ls = g.lane_scale ? g.lane_scale[f] : 1.f;
+  const float bias = g.bias ? g.bias[f] : 0.f;
+  const int n = min(16, g.T - t0);
+  float res[16];
+  if (g.residual) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < n) res[j] = load_out(g.residual, (long long)(t0 + j) * g.F + f, g.out_type);
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= n) continue;
+    const long long at = (long long)(t0 + j) * g.F + f;
+    float v = acc[j];
+    if (g.lane_scale) v *= ls * g.col_scale[t0 + j];
+    v += bias;
+    if (g.pre) store_out(g.pre, at, g.out_type, v);
+    v = activate(v, g.act);
+    if (g.residual) v += res[j];
+    store_out(g.out, at, g.out_type, v);
+  }
+}
+
+// ORs a flag over the epilogue's threads (and is their barrier).
+__device__ __forceinline__ bool epi_any(bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)flag)
+      : "memory");
+  return r != 0;
+}
+
+// A_MN / B_MN: the operand is contiguous along lanes / columns, not along the contraction.
+template <bool F8, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm g) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (su32(smem) & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) report(g.status, DSPARK_STATUS_INTERNAL, 0);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* last_flag = abort_flag + 1;
+  volatile int* dead = abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stage_bytes = kABytes + g.nt * 128;
+  const int stages = min(kMaxStages, kRing / stage_bytes);
+  const int units = g.tiles_f * g.tiles_t * g.splits;
+  // unit u: part u % splits of tile u / splits; tiles run over the columns first,
+  // so that CTAs working at the same time share their rows of A
+  auto blocks = [&](int u, int& k0, int& k1) {
+    const int sp = u % g.splits;
+    k0 = (int)((long long)g.kblocks * sp / g.splits);
+    k1 = (int)((long long)g.kblocks * (sp + 1) / g.splits);
+  };
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiThreads);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {  // two accumulators of 256 columns
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0, last = -1;
+      for (int u = blockIdx.x; u < units && !*dead; u += gridDim.x) {
+        const int tile = u / g.splits;
+        const int f0 = tile / g.tiles_t * kTileF, t0 = tile % g.tiles_t * g.nt;
+        int k0, k1;
+        blocks(u, k0, k1);
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const int s = it % stages;
+          if (!mbar_wait_bounded(su32(&empty[s]), ((it / stages) & 1) ^ 1)) {
+            if (!*dead) report_wait(g.status, kWhereEmpty, 0);
+            *dead = 1;
+            break;
+          }
+          mbar_expect_tx(&full[s], stage_bytes);
+          const uint32_t a = su32(smem) + s * stage_bytes, b = a + kABytes;
+          const int kx = kb * (F8 ? 128 : 64);
+          if (A_MN) {
+            tma_load_2d(a, &map_a, f0, kx, &full[s]);
+            tma_load_2d(a + kBoxBytes, &map_a, f0 + 64, kx, &full[s]);
+          } else {
+            tma_load_2d(a, &map_a, kx, f0, &full[s]);
+          }
+          if (B_MN) {
+            for (int q = 0; q < g.nt / 64; ++q) tma_load_2d(b + q * kBoxBytes, &map_b, t0 + q * 64, kx, &full[s]);
+          } else {
+            tma_load_2d(b, &map_b, kx, t0, &full[s]);
+          }
+          last = it;
+        }
+      }
+      if (*dead)  // let issued loads land before the CTA winds down
+        for (int q = max(0, last - stages + 1); q <= last; ++q)
+          mbar_wait_bounded(su32(&full[q % stages]), (q / stages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // D fp32; A and B bf16 or e4m3; widths nt and 128
+      const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) |
+                             ((uint32_t)B_MN << 16) | ((uint32_t)(g.nt >> 3) << 17) | ((uint32_t)(kTileF >> 4) << 24);
+      int it = 0, ti = 0;
+      for (int u = blockIdx.x; u < units && !*dead; u += gridDim.x, ++ti) {
+        const int buf = ti & 1;
+        if (!mbar_wait_bounded(su32(&acc_empty[buf]), ((ti >> 1) & 1) ^ 1)) {
+          if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
+          *dead = 1;
+          break;
+        }
+        fence_after();
+        int k0, k1;
+        blocks(u, k0, k1);
+        const uint32_t d = tmem + buf * kMaxCols;
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const int s = it % stages;
+          if (!mbar_wait_bounded(su32(&full[s]), (it / stages) & 1)) {
+            if (!*dead) report_wait(g.status, kWhereFull, 0);
+            *dead = 1;
+            break;
+          }
+          fence_after();
+          const uint32_t a = su32(smem) + s * stage_bytes, b = a + kABytes;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // 32 bytes of the contraction (or 16 rows of it) each
+            const uint64_t ad = A_MN ? sdesc(a + q * 2048, kBoxBytes, 1024) : sdesc(a + q * 32, 16, 1024);
+            const uint64_t bd = B_MN ? sdesc(b + q * 2048, kBoxBytes, 1024) : sdesc(b + q * 32, 16, 1024);
+            mma<F8>(d, ad, bd, idesc, kb > k0 || q > 0);
+          }
+          mma_commit(&empty[s]);
+        }
+        if (*dead) break;
+        mma_commit(&acc_full[buf]);
+      }
+      if (*dead && it > 0)  // MMAs complete in order: after the last commit tensor memory is quiet
+        mbar_wait_bounded(su32(&empty[(it - 1) % stages]), ((it - 1) / stages) & 1);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int fl = quarter * 32 + lane;  // lane of the tile
+    int ti = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++ti) {
+      const int buf = ti & 1, tile = u / g.splits, sp = u % g.splits;
+      const int f = tile / g.tiles_t * kTileF + fl, t0 = tile % g.tiles_t * g.nt;
+      const bool ok = !*dead && mbar_wait_bounded(su32(&acc_full[buf]), (ti >> 1) & 1);
+      if (epi_any(!ok)) {
+        if (tid == 64 && !*dead) report_wait(g.status, kWhereAccFull, 0);
+        *dead = 1;
+        break;
+      }
+      fence_after();
+      const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
+      float* part = g.splits > 1 ? g.partial + (size_t)tile * g.splits * g.nt * kTileF : nullptr;
+      for (int c = half * 16; c < g.nt; c += 32) {
+        if (t0 + c >= g.T) break;
+        float v[16];
+        tmem_ld16(src + c, v);
+        if (!part) {
+          finish16(g, v, f, t0 + c);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[((size_t)sp * g.nt + c + j) * kTileF + fl] = v[j];
+        }
+      }
+      fence_before();
+      mbar_arrive(&acc_empty[buf]);
+      if (part) {
+        __threadfence();
+        epi_any(false);
+        if (tid == 64) *last_flag = atomicAdd(&g.counter[tile], 1u) == (unsigned)g.splits - 1;
+        epi_any(false);
+        if (*(volatile int*)last_flag) {
+          __threadfence();
+          for (int c = half * 16; c < g.nt; c += 32) {
+            if (t0 + c >= g.T) break;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+            for (int q = 0; q < g.splits; ++q)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] += __ldcg(&part[((size_t)q * g.nt + c + j) * kTileF + fl]);
+            finish16(g, v, f, t0 + c);
+          }
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// dpre = round_bf16(dy act'(pre)) (the tensor cores take bf16 operands; the
+// rounding is half a bf16 step of each factor, as in the bf16 result) and
+// per-CTA column sums of the unrounded values. A CTA takes 256 columns and a
+// contiguous run of rows, 8 rows at a time.
+constexpr int kDpreRows = 8;
+
+__global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* pre, int M, int N, int act, int rows_per,
+                                                   void* dpre, float* partial) {
+  __shared__ float part[kDpreRows][256 + 8];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int n0 = blockIdx.x * 256 + lane * 8;
+  const int m1 = min(M, (int)(blockIdx.y + 1) * rows_per);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (n0 < N) {
+    for (int m = blockIdx.y * rows_per + row; m < m1; m += kDpreRows) {
+      const size_t at = ((size_t)m * N + n0) * 2;
+      float d[8];
+      Vec16<DSPARK_BF16>::load(static_cast<const char*>(dy) + at, d);
+      if (act != DSPARK_ACT_NONE) {
+        float z[8];
+        Vec16<DSPARK_BF16>::load(static_cast<const char*>(pre) + at, z);
+        alignas(16) uint16_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[e] *= activate_grad(z[e], act);
+          o[e] = Elem<DSPARK_BF16>::store_round(d[e]);
+        }
+        *reinterpret_cast<uint4*>(static_cast<char*>(dpre) + at) = *reinterpret_cast<const uint4*>(o);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += d[e];
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[row][lane * 8 + e] = acc[e];
+  __syncthreads();
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n < N) {
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < kDpreRows; ++q) t += part[q][threadIdx.x];
+    partial[(size_t)blockIdx.y * N + n] = t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host: how the work is cut
+// ---------------------------------------------------------------------------
+struct Plan {
+  int nt, tiles_f, tiles_t, splits;
+  size_t partial_bytes() const {
+    return splits > 1 ? (size_t)tiles_f * tiles_t * splits * nt * kTileF * sizeof(float) : 0;
+  }
+  size_t counter_bytes() const { return splits > 1 ? round_up((size_t)tiles_f * tiles_t * sizeof(unsigned int), 256) : 0; }
+  size_t bytes() const { return counter_bytes() + round_up(partial_bytes(), 256); }
+};
+
+// The column width and the split of the contraction with the least time by a
+// count of cycles: a 128-byte block of a stage costs its bytes at 64 a cycle or
+// its matrix instructions (nt / 2 cycles each), whichever is more; a unit adds
+// a fixed start and end.
+Plan make_plan(long long F, long long T, int kblocks, int min_nt) {
+  Plan best = {};
+  double best_cost = 1e300;
+  for (int nt = min_nt; nt <= kMaxCols; nt *= 2) {
+    Plan p;
+    p.nt = nt;
+    p.tiles_f = (int)((F + kTileF - 1) / kTileF);
+    p.tiles_t = (int)((T + nt - 1) / nt);
+    const long long tiles = (long long)p.tiles_f * p.tiles_t;
+    p.splits = (int)(tiles < kPlanSms ? kPlanSms / tiles : 1);
+    if (p.splits > kblocks / 4) p.splits = kblocks / 4;
+    if (p.splits < 1) p.splits = 1;
+    const long long waves = (tiles * p.splits + kPlanSms - 1) / kPlanSms;
+    const double block = fmax((kABytes + nt * 128) / 64.0, 2.0 * nt);
+    const double unit = (double)((kblocks + p.splits - 1) / p.splits) * block + 1500 + 8.0 * nt * (p.splits > 1 ? 2 : 1);
+    const double cost = waves * unit;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+
+inline int kblocks_of(long long bytes_or_rows, int per) { return (int)((bytes_or_rows + per - 1) / per); }
+
+Plan plan_forward(int M, int N, int K, int in_type) {
+  return make_plan(N, M, in_type == DSPARK_E4M3 ? kblocks_of(K, 128) : kblocks_of(K, 64), 16);
+}
+Plan plan_dx(int M, int N, int K) { return make_plan(K, M, kblocks_of(N, 64), 16); }
+Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), 64); }
+
+// Row runs of dpre_kernel: enough CTAs for two on every SM, 64 rows or more each.
+inline int dpre_runs(int M, int N) {
+  const int cols = (N + 255) / 256;
+  return max(1, min((M + 63) / 64, (2 * kPlanSms + cols - 1) / cols));
+}
+
+template <bool F8, bool A_MN, bool B_MN>
+cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, char* scratch, int num_sms,
+                        cudaStream_t s) {
+  g.nt = p.nt;
+  g.tiles_f = p.tiles_f;
+  g.tiles_t = p.tiles_t;
+  g.splits = p.splits;
+  cudaError_t e;
+  if (p.splits > 1) {
+    g.counter = reinterpret_cast<unsigned int*>(scratch);
+    g.partial = reinterpret_cast<float*>(scratch + p.counter_bytes());
+    e = cudaMemsetAsync(g.counter, 0, p.counter_bytes(), s);
+    if (e != cudaSuccess) return e;
+  }
+  auto kern = linear_kernel<F8, A_MN, B_MN>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)p.tiles_f * p.tiles_t * p.splits;
+  kern<<<(unsigned)min(units, (long long)num_sms), kThreads, kSmem, s>>>(ma, mb, g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t linear_scratch_bytes(int M, int N, int K, int in_type) {
+  size_t n = plan_forward(M, N, K, in_type).bytes();
+  if (in_type == DSPARK_BF16) {
+    const size_t split = max(plan_dx(M, N, K).bytes(), plan_dw(M, N, K).bytes());
+    const size_t grad = split + round_up((size_t)M * N * 2, 256) + round_up((size_t)dpre_runs(M, N) * N * sizeof(float), 256);
+    if (grad > n) n = grad;
+  }
+  return n;
+}
+
+cudaError_t linear_launch(const LinearArgs& a, int num_sms, cudaStream_t s) {
+  const bool f8 = a.in_type == DSPARK_E4M3;
+  const int es = f8 ? 1 : 2;
+  const Plan p = plan_forward(a.M, a.N, a.K, a.in_type);
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, a.w, es, a.K, a.N, kTileF) || !make_map(&mb, a.x, es, a.K, a.M, p.nt)) return cudaErrorInvalidValue;
+  Gemm g = {};
+  g.F = a.N;
+  g.T = a.M;
+  g.kblocks = kblocks_of((long long)a.K * es, 128);
+  g.col_scale = a.x_scale;
+  g.lane_scale = a.w_scale;
+  g.bias = a.bias;
+  g.residual = a.residual;
+  g.out = a.y;
+  g.pre = a.pre;
+  g.out_type = a.out_type;
+  g.act = a.act;
+  g.status = a.status;
+  return f8 ? gemm_launch<true, false, false>(g, p, ma, mb, a.scratch, num_sms, s)
+            : gemm_launch<false, false, false>(g, p, ma, mb, a.scratch, num_sms, s);
+}
+
+cudaError_t linear_grad_launch(const LinearGradArgs& a, int num_sms, cudaStream_t s) {
+  const Plan px = plan_dx(a.M, a.N, a.K), pw = plan_dw(a.M, a.N, a.K);
+  char* split = a.scratch;
+  char* dpre_buf = split + max(px.bytes(), pw.bytes());
+  float* partial = reinterpret_cast<float*>(dpre_buf + round_up((size_t)a.M * a.N * 2, 256));
+  const void* dpre = a.act == DSPARK_ACT_NONE ? a.dy : dpre_buf;
+  cudaError_t e;
+  if (a.act != DSPARK_ACT_NONE || a.dbias) {
+    const int runs = dpre_runs(a.M, a.N);
+    const int rows_per = (a.M + runs - 1) / runs;
+    dpre_kernel<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, a.act, rows_per, dpre_buf,
+                                                              a.dbias ? partial : nullptr);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.dbias && (e = column_sums_launch(partial, runs, a.N, a.dbias, s)) != cudaSuccess) return e;
+  }
+  CUtensorMap ma, mb;
+  Gemm g = {};
+  g.F = a.K;
+  g.out_type = DSPARK_BF16;
+  g.act = DSPARK_ACT_NONE;
+  g.status = a.status;
+  if (a.dx) {  // lanes k, columns m, contraction n
+    if (!make_map(&ma, a.w, 2, a.K, a.N, 64) || !make_map(&mb, dpre, 2, a.N, a.M, px.nt)) return cudaErrorInvalidValue;
+    g.T = a.M;
+    g.kblocks = kblocks_of(a.N, 64);
+    g.out = a.dx;
+    if ((e = gemm_launch<false, true, false>(g, px, ma, mb, split, num_sms, s)) != cudaSuccess) return e;
+  }
+  if (a.dw) {  // lanes k, columns n, contraction m
+    if (!make_map(&ma, a.x, 2, a.K, a.M, 64) || !make_map(&mb, dpre, 2, a.N, a.M, 64)) return cudaErrorInvalidValue;
+    g.T = a.N;
+    g.kblocks = kblocks_of(a.M, 64);
+    g.out = a.dw;
+    if ((e = gemm_launch<false, true, true>(g, pw, ma, mb, split, num_sms, s)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace dspark
