@@ -116,6 +116,9 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None,
     """
     if t is None:
         return None
+    if ((dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and t.device == device and t.is_contiguous()):
+        return t.data_ptr()  # the usual case: a call's host time is mostly these checks
     if dtype is not None and t.dtype != dtype:
         raise DSparkError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -136,11 +139,18 @@ def _on_gpu(device: torch.device) -> None:
         raise DSparkError(f"the call's tensors must be CUDA tensors, not on {device}")
 
 
+# The handle of a device's current stream without building a Stream object
+# (0.1 us in place of 2 us per call).
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device: torch.device) -> int:
     """The handle of `stream`, or of `device`'s current stream; a stream of
     another device is refused (its kernels would run there with this
     device's pointers)."""
     if stream is None:
+        if _current_handle is not None and device.index is not None:
+            return _current_handle(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     if stream.device != device:
         raise DSparkError(f"the stream is on {stream.device}, the call's tensors on {device}")
@@ -153,9 +163,14 @@ def _call(name: str, device: torch.device, args, stream) -> None:
     the device that holds the call's tensors."""
     _on_gpu(device)
     s = _stream(stream, device)
-    with torch.cuda.device(device):
-        rc = getattr(lib(), name)(*args, s)
-    _check(rc, name)
+    fn = getattr(_lib if _lib is not None else lib(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc != 0:
+        _check(rc, name)
 
 
 def workspace_bytes(op: int, B: int, K: int, V: int, r: int, dtype: int) -> int:

@@ -1,6 +1,8 @@
 // Host-side helpers shared by the C ABI's translation units.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace dspark {
@@ -30,16 +32,24 @@ inline bool linear_shape_ok(int M, int N, int K, int in_type) {
 }
 
 // DSPARK_OK on a device of compute capability 10.0 (the fatbin carries sm_100a
-// code only), and its SM count.
+// code only), and its SM count. Both are fixed for the life of the process, so
+// each device is asked once (a query costs a call about 1 us of host time).
 inline int device_check(int* num_sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0 unknown, -1 unsupported, else the SM count
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
-  if (major != 10 || minor != 0) return DSPARK_ERR_UNSUPPORTED;
+  int sms = dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return DSPARK_ERR_CUDA;
+    if (major != 10 || minor != 0) sms = -1;
+    if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+  }
+  if (sms < 0) return DSPARK_ERR_UNSUPPORTED;
   if (num_sms) *num_sms = sms;
   return DSPARK_OK;
 }
