@@ -15,13 +15,18 @@
 //   dx [m, k]: lanes k, A = w (k = lanes contiguous), columns m, B = dpre (n contiguous)
 //   dw [n, k]: lanes k, A = x (k = lanes contiguous), columns n, B = dpre (n = columns contiguous)
 //
-// Persistent CTAs take work units (output tile, part of the contraction):
-//   warp 0     TMA producer: 128-byte-wide boxes of A and B into a ring of stages
-//   warp 1     tensor-memory allocation and the single-thread tcgen05.mma issuer
+// Persistent pairs of CTAs (cta_group::2: one matrix instruction of 256 lanes
+// uses both SMs' tensor cores, each SM holding its 128 lanes of A and of the
+// result and half of B's columns, so every B byte enters one SM only) take work
+// units (output tile, part of the contraction):
+//   warp 0     TMA producer: 128-byte-wide boxes of this CTA's A and B into a ring
+//              of stages; the bytes of both CTAs complete on the first one's barrier
+//   warp 1     tensor-memory allocation and, in the first CTA, the single-thread
+//              tcgen05.mma issuer
 //   warps 2-9  epilogue of the previous unit meanwhile (two accumulators): a warp
 //              reads its quarter of the lanes (hardware: warp index mod 4), the two
 //              halves take alternate blocks of 16 columns
-// With fewer tiles than SMs the contraction is split: each part leaves its fp32
+// With fewer tiles than pairs the contraction is split: each part leaves its fp32
 // sums in the workspace and the last to arrive adds them in order of the parts
 // (the result does not depend on who that is) and finishes the tile.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
@@ -38,9 +43,10 @@ using namespace t5;
 
 constexpr int kThreads = 320;
 constexpr int kEpiThreads = 256;
-constexpr int kTileF = 128;                    // lanes: output features per tile
+constexpr int kTileF = 256;                    // lanes: output features per tile, 128 in each CTA of the pair
+constexpr int kLanes = 128;
 constexpr int kMaxCols = 256;                  // columns per tile at most
-constexpr int kABytes = kTileF * 128;          // A of a stage: 128 bytes of contraction (or lanes) x 128
+constexpr int kABytes = kLanes * 128;          // A of a stage: 128 bytes of contraction (or lanes) x 128
 constexpr int kMaxStages = 12;
 constexpr int kRing = 221184;                  // bytes of the stage ring (216 KB)
 constexpr int kBoxBytes = 64 * 128;            // one [64 x 128 bytes] box of a lane- or column-contiguous operand
@@ -48,7 +54,7 @@ constexpr int kOffBar = kRing;
 constexpr int kNumBars = 2 * kMaxStages + 4;
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
 static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory per block");
-constexpr int kPlanSms = 148;                  // SMs that the split of the work is planned for
+constexpr int kPlanPairs = 74;                 // pairs of SMs that the split of the work is planned for
 
 enum : unsigned int {  // wait sites recorded when a bounded wait gives up
   kWhereEmpty = 40,
@@ -60,7 +66,7 @@ enum : unsigned int {  // wait sites recorded when a bounded wait gives up
 struct Gemm {
   int F, T;                 // lanes (contiguous outputs) and columns in all
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
-  int nt;                   // columns per tile, a multiple of 16 (64 when B is column-contiguous)
+  int nt;                   // columns per tile, a multiple of 16 (128 when B is column-contiguous)
   int tiles_f, tiles_t, splits;
   const float* col_scale;   // [T] or null
   const float* lane_scale;  // [F] or null
@@ -69,8 +75,8 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  float* partial;           // [tile, split, nt, 128] (splits > 1)
-  unsigned int* counter;    // [tile], zero at launch (splits > 1)
+  float* partial;           // [tile, split, nt, 256] (splits > 1)
+  unsigned int* counter;    // [tile, CTA of the pair], zero at launch (splits > 1)
   Status* status;
 };
 
@@ -109,29 +115,43 @@ __device__ __forceinline__ void store_out(void* p, long long i, int type, float 
 }
 
 // 16 columns of one lane: scales, bias, activation, residual, rounding, stores.
-__device__ __forceinline__ void finish16(const Gemm& g, const float* acc, int f, int t0) {
+// Everything is loaded before the first store: a load behind a store that might
+// alias it waits for its turn (25 us a tile instead of the 2 us measured so).
+__device__ __forceinline__ void finish16(const Gemm& g, float* v, int f, int t0) {
   if (f >= g.F) return;
-  const float ls = g.lane_scale ? g.lane_scale[f] : 1.f;
-  const float bias = g.bias ? g.bias[f] : 0.f;
   const int n = min(16, g.T - t0);
+  const long long at = (long long)t0 * g.F + f;
   float res[16];
   if (g.residual) {
 #pragma unroll
+    for (int j = 0; j < 16; ++j) res[j] = j < n ? load_out(g.residual, at + (long long)j * g.F, g.out_type) : 0.f;
+  }
+  if (g.lane_scale) {
+    const float ls = __ldg(g.lane_scale + f);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= ls * (j < n ? __ldg(g.col_scale + t0 + j) : 0.f);
+  }
+  if (g.bias) {
+    const float bias = __ldg(g.bias + f);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += bias;
+  }
+  if (g.pre) {
+#pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (j < n) res[j] = load_out(g.residual, (long long)(t0 + j) * g.F + f, g.out_type);
+      if (j < n) store_out(g.pre, at + (long long)j * g.F, g.out_type, v[j]);
+  }
+  if (g.act != DSPARK_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], g.act);
+  }
+  if (g.residual) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += res[j];
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (j >= n) continue;
-    const long long at = (long long)(t0 + j) * g.F + f;
-    float v = acc[j];
-    if (g.lane_scale) v *= ls * g.col_scale[t0 + j];
-    v += bias;
-    if (g.pre) store_out(g.pre, at, g.out_type, v);
-    v = activate(v, g.act);
-    if (g.residual) v += res[j];
-    store_out(g.out, at, g.out_type, v);
-  }
+  for (int j = 0; j < 16; ++j)
+    if (j < n) store_out(g.out, at + (long long)j * g.F, g.out_type, v[j]);
 }
 
 // ORs a flag over the epilogue's threads (and is their barrier).
@@ -147,10 +167,10 @@ __device__ __forceinline__ bool epi_any(bool flag) {
 
 // A_MN / B_MN: the operand is contiguous along lanes / columns, not along the contraction.
 template <bool F8, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm g) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  if (su32(smem) & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment
+  if (su32(smem) & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment (the same offset in every CTA)
     if (threadIdx.x == 0) report(g.status, DSPARK_STATUS_INTERNAL, 0);
     return;
   }
@@ -164,11 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* dead = abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int stage_bytes = kABytes + g.nt * 128;
+  const uint32_t rank = cta_rank();
+  const int nh = g.nt / 2;  // columns of B in this CTA
+  const int stage_bytes = kABytes + nh * 128;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int stages = min(kMaxStages, kRing / stage_bytes);
   const int units = g.tiles_f * g.tiles_t * g.splits;
   // unit u: part u % splits of tile u / splits; tiles run over the columns first,
-  // so that CTAs working at the same time share their rows of A
+  // so that pairs working at the same time share their rows of A
   auto blocks = [&](int u, int& k0, int& k1) {
     const int sp = u % g.splits;
     k0 = (int)((long long)g.kblocks * sp / g.splits);
@@ -182,26 +205,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiThreads);
+      mbar_init(&acc_empty[i], 2 * kEpiThreads / 32);  // a warp of either CTA each
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {  // two accumulators of 256 columns
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   fence_before();
-  __syncthreads();
+  cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     if (lane == 0) {
       int it = 0, last = -1;
-      for (int u = blockIdx.x; u < units && !*dead; u += gridDim.x) {
+      for (int u = pair; u < units && !*dead; u += pairs) {
         const int tile = u / g.splits;
-        const int f0 = tile / g.tiles_t * kTileF, t0 = tile % g.tiles_t * g.nt;
+        const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt + rank * nh;
         int k0, k1;
         blocks(u, k0, k1);
         for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -211,35 +234,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             *dead = 1;
             break;
           }
-          mbar_expect_tx(&full[s], stage_bytes);
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
+          const uint32_t bar = map_rank(su32(&full[s]), 0);
           const uint32_t a = su32(smem) + s * stage_bytes, b = a + kABytes;
           const int kx = kb * (F8 ? 128 : 64);
           if (A_MN) {
-            tma_load_2d(a, &map_a, f0, kx, &full[s]);
-            tma_load_2d(a + kBoxBytes, &map_a, f0 + 64, kx, &full[s]);
+            tma_load_2d(a, &map_a, f0, kx, bar);
+            tma_load_2d(a + kBoxBytes, &map_a, f0 + 64, kx, bar);
           } else {
-            tma_load_2d(a, &map_a, kx, f0, &full[s]);
+            tma_load_2d(a, &map_a, kx, f0, bar);
           }
           if (B_MN) {
-            for (int q = 0; q < g.nt / 64; ++q) tma_load_2d(b + q * kBoxBytes, &map_b, t0 + q * 64, kx, &full[s]);
+            for (int q = 0; q < nh / 64; ++q) tma_load_2d(b + q * kBoxBytes, &map_b, t0 + q * 64, kx, bar);
           } else {
-            tma_load_2d(b, &map_b, kx, t0, &full[s]);
+            tma_load_2d(b, &map_b, kx, t0, bar);
           }
           last = it;
         }
       }
-      if (*dead)  // let issued loads land before the CTA winds down
+      if (*dead && rank == 0)  // let issued loads of both CTAs land before the pair winds down (below)
         for (int q = max(0, last - stages + 1); q <= last; ++q)
           mbar_wait_bounded(su32(&full[q % stages]), (q / stages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // D fp32; A and B bf16 or e4m3; widths nt and 128
+    if (lane == 0 && rank == 0) {
+      // D fp32; A and B bf16 or e4m3; widths nt and 256
       const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) |
                              ((uint32_t)B_MN << 16) | ((uint32_t)(g.nt >> 3) << 17) | ((uint32_t)(kTileF >> 4) << 24);
       int it = 0, ti = 0;
-      for (int u = blockIdx.x; u < units && !*dead; u += gridDim.x, ++ti) {
+      for (int u = pair; u < units && !*dead; u += pairs, ++ti) {
         const int buf = ti & 1;
         if (!mbar_wait_bounded(su32(&acc_empty[buf]), ((ti >> 1) & 1) ^ 1)) {
           if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
@@ -276,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int fl = quarter * 32 + lane;  // lane of the tile
+    const int fl = rank * kLanes + quarter * 32 + lane;  // lane of the tile
+    const uint32_t acc_free[2] = {map_rank(su32(&acc_empty[0]), 0), map_rank(su32(&acc_empty[1]), 0)};
     int ti = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++ti) {
+    for (int u = pair; u < units; u += pairs, ++ti) {
       const int buf = ti & 1, tile = u / g.splits, sp = u % g.splits;
       const int f = tile / g.tiles_t * kTileF + fl, t0 = tile % g.tiles_t * g.nt;
       const bool ok = !*dead && mbar_wait_bounded(su32(&acc_full[buf]), (ti >> 1) & 1);
@@ -302,11 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       fence_before();
-      mbar_arrive(&acc_empty[buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_free[buf]);
       if (part) {
         __threadfence();
         epi_any(false);
-        if (tid == 64) *last_flag = atomicAdd(&g.counter[tile], 1u) == (unsigned)g.splits - 1;
+        if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * tile + rank], 1u) == (unsigned)g.splits - 1;
         epi_any(false);
         if (*(volatile int*)last_flag) {
           __threadfence();
@@ -325,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   fence_before();
-  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other's arrivals or loads may still reach it
   fence_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // dpre = round_bf16(dy act'(pre)) (the tensor cores take bf16 operands; the
@@ -384,7 +410,7 @@ struct Plan {
   size_t partial_bytes() const {
     return splits > 1 ? (size_t)tiles_f * tiles_t * splits * nt * kTileF * sizeof(float) : 0;
   }
-  size_t counter_bytes() const { return splits > 1 ? round_up((size_t)tiles_f * tiles_t * sizeof(unsigned int), 256) : 0; }
+  size_t counter_bytes() const { return splits > 1 ? round_up((size_t)tiles_f * tiles_t * 2 * sizeof(unsigned int), 256) : 0; }
   size_t bytes() const { return counter_bytes() + round_up(partial_bytes(), 256); }
 };
 
@@ -401,11 +427,11 @@ Plan make_plan(long long F, long long T, int kblocks, int min_nt) {
     p.tiles_f = (int)((F + kTileF - 1) / kTileF);
     p.tiles_t = (int)((T + nt - 1) / nt);
     const long long tiles = (long long)p.tiles_f * p.tiles_t;
-    p.splits = (int)(tiles < kPlanSms ? kPlanSms / tiles : 1);
+    p.splits = (int)(tiles < kPlanPairs ? kPlanPairs / tiles : 1);
     if (p.splits > kblocks / 4) p.splits = kblocks / 4;
     if (p.splits < 1) p.splits = 1;
-    const long long waves = (tiles * p.splits + kPlanSms - 1) / kPlanSms;
-    const double block = fmax((kABytes + nt * 128) / 64.0, 2.0 * nt);
+    const long long waves = (tiles * p.splits + kPlanPairs - 1) / kPlanPairs;
+    const double block = fmax((kABytes + nt * 64) / 64.0, 2.0 * nt);
     const double unit = (double)((kblocks + p.splits - 1) / p.splits) * block + 1500 + 8.0 * nt * (p.splits > 1 ? 2 : 1);
     const double cost = waves * unit;
     if (cost < best_cost) {
@@ -422,12 +448,12 @@ Plan plan_forward(int M, int N, int K, int in_type) {
   return make_plan(N, M, in_type == DSPARK_E4M3 ? kblocks_of(K, 128) : kblocks_of(K, 64), 16);
 }
 Plan plan_dx(int M, int N, int K) { return make_plan(K, M, kblocks_of(N, 64), 16); }
-Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), 64); }
+Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), 128); }
 
 // Row runs of dpre_kernel: enough CTAs for two on every SM, 64 rows or more each.
 inline int dpre_runs(int M, int N) {
   const int cols = (N + 255) / 256;
-  return max(1, min((M + 63) / 64, (2 * kPlanSms + cols - 1) / cols));
+  return max(1, min((M + 63) / 64, (4 * kPlanPairs + cols - 1) / cols));
 }
 
 template <bool F8, bool A_MN, bool B_MN>
@@ -448,7 +474,7 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.tiles_f * p.tiles_t * p.splits;
-  kern<<<(unsigned)min(units, (long long)num_sms), kThreads, kSmem, s>>>(ma, mb, g);
+  kern<<<2 * (unsigned)min(units, (long long)num_sms / 2), kThreads, kSmem, s>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
@@ -469,7 +495,7 @@ cudaError_t linear_launch(const LinearArgs& a, int num_sms, cudaStream_t s) {
   const int es = f8 ? 1 : 2;
   const Plan p = plan_forward(a.M, a.N, a.K, a.in_type);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a.w, es, a.K, a.N, kTileF) || !make_map(&mb, a.x, es, a.K, a.M, p.nt)) return cudaErrorInvalidValue;
+  if (!make_map(&ma, a.w, es, a.K, a.N, kLanes) || !make_map(&mb, a.x, es, a.K, a.M, p.nt / 2)) return cudaErrorInvalidValue;
   Gemm g = {};
   g.F = a.N;
   g.T = a.M;
@@ -510,7 +536,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, int num_sms, cudaStream_
   g.act = DSPARK_ACT_NONE;
   g.status = a.status;
   if (a.dx) {  // lanes k, columns m, contraction n
-    if (!make_map(&ma, a.w, 2, a.K, a.N, 64) || !make_map(&mb, dpre, 2, a.N, a.M, px.nt)) return cudaErrorInvalidValue;
+    if (!make_map(&ma, a.w, 2, a.K, a.N, 64) || !make_map(&mb, dpre, 2, a.N, a.M, px.nt / 2)) return cudaErrorInvalidValue;
     g.T = a.M;
     g.kblocks = kblocks_of(a.N, 64);
     g.out = a.dx;
