@@ -7,9 +7,7 @@
 // Orientation: the matrix instruction's 128 rows (tensor-memory lanes) are the
 // output's contiguous index (features), its columns the other one (tokens).
 // One kernel then serves one token and thousands: the column tile is 16 to 256
-// wide, a small batch streams the weights past a few columns, and a warp's
-// store of one column is 32 neighbouring outputs, so the epilogue needs no
-// staging and no alignment of the output's width. The three products differ
+// wide, and a small batch streams the weights past a few columns. The three products differ
 // only in which operand lies contraction-major:
 //   y  [m, n]: lanes n, A = w (k contiguous),  columns m, B = x    (k contiguous)
 //   dx [m, k]: lanes k, A = w (k = lanes contiguous), columns m, B = dpre (n contiguous)
@@ -48,9 +46,13 @@ constexpr int kLanes = 128;
 constexpr int kMaxCols = 256;                  // columns per tile at most
 constexpr int kABytes = kLanes * 128;          // A of a stage: 128 bytes of contraction (or lanes) x 128
 constexpr int kMaxStages = 12;
-constexpr int kRing = 221184;                  // bytes of the stage ring (216 KB)
+constexpr int kRing = 6 * 32768;               // bytes of the stage ring
 constexpr int kBoxBytes = 64 * 128;            // one [64 x 128 bytes] box of a lane- or column-contiguous operand
-constexpr int kOffBar = kRing;
+constexpr int kChunk = 32;                     // columns that one half of the epilogue takes at a time
+constexpr int kPitch = kLanes + 8;             // entries of a staged row: 8 rows of 16 bytes fall on all banks
+constexpr int kOffStage = kRing;
+constexpr int kOffScale = kOffStage + 2 * kChunk * kPitch * 2;  // col_scale of the tile, two buffers
+constexpr int kOffBar = kOffScale + 2 * kMaxCols * 4;
 constexpr int kNumBars = 2 * kMaxStages + 4;
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
 static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory per block");
@@ -75,7 +77,8 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  float* partial;           // [tile, split, nt, 256] (splits > 1)
+  int staged;               // bf16 outputs, aligned alike: through shared memory
+  float* partial;           // [tile, split, 2, nt rounded up to 32, 128] (splits > 1)
   unsigned int* counter;    // [tile, CTA of the pair], zero at launch (splits > 1)
   Status* status;
 };
@@ -114,44 +117,103 @@ __device__ __forceinline__ void store_out(void* p, long long i, int type, float 
     static_cast<uint16_t*>(p)[i] = Elem<DSPARK_BF16>::store_round(v);
 }
 
-// 16 columns of one lane: scales, bias, activation, residual, rounding, stores.
-// Everything is loaded before the first store: a load behind a store that might
-// alias it waits for its turn (25 us a tile instead of the 2 us measured so).
-__device__ __forceinline__ void finish16(const Gemm& g, float* v, int f, int t0) {
+__device__ __forceinline__ void activate32(float* v, int act) {
+  if (act != DSPARK_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], act);
+  }
+}
+
+// fp32 outputs (and 2-byte tensors that are not aligned alike): one lane's
+// columns straight to memory, 32 neighbouring outputs per warp and store. All
+// loads come before the first store: a load behind a store that might alias it
+// waits for its turn.
+__device__ __forceinline__ void direct32(const Gemm& g, float* v, int f, int t0, int cols) {
   if (f >= g.F) return;
-  const int n = min(16, g.T - t0);
+  const int n = min(cols, g.T - t0);
   const long long at = (long long)t0 * g.F + f;
-  float res[16];
-  if (g.residual) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) res[j] = j < n ? load_out(g.residual, at + (long long)j * g.F, g.out_type) : 0.f;
-  }
-  if (g.lane_scale) {
-    const float ls = __ldg(g.lane_scale + f);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= ls * (j < n ? __ldg(g.col_scale + t0 + j) : 0.f);
-  }
-  if (g.bias) {
-    const float bias = __ldg(g.bias + f);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += bias;
-  }
   if (g.pre) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 32; ++j)
       if (j < n) store_out(g.pre, at + (long long)j * g.F, g.out_type, v[j]);
   }
-  if (g.act != DSPARK_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], g.act);
-  }
+  activate32(v, g.act);
   if (g.residual) {
+    float res[32];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += res[j];
+    for (int j = 0; j < 32; ++j) res[j] = j < n ? load_out(g.residual, at + (long long)j * g.F, g.out_type) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += res[j];
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < 32; ++j)
     if (j < n) store_out(g.out, at + (long long)j * g.F, g.out_type, v[j]);
+}
+
+__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory"); }
+
+// bf16 outputs go through shared memory: a lane holds one feature of many
+// tokens, memory wants many features of one token. Row j of the stage holds the
+// 128 features of token t0 + j. Between stage and memory rows move as 16-byte
+// vectors of the memory's alignment: 16 of them where the width is a multiple of
+// 8 entries, else (any width, any 2-byte alignment) up to 17, the vectors inside
+// the row read from the stage at their odd offset, up to 7 entries singly at
+// either end. `rows` tokens from t0, features f0 .. f0 + nf - 1; 128 threads (th).
+template <bool STORE>
+__device__ __forceinline__ void move_rows(const Gemm& g, uint16_t* stage, void* p, int f0, int nf, int t0, int rows, int th) {
+  uint16_t* base = static_cast<uint16_t*>(p) + (long long)t0 * g.F + f0;
+  if ((g.F & 7) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const int e = (th & 15) * 8;
+    if (e >= nf) return;
+    uint16_t* s = stage + (th >> 4) * kPitch + e;
+    uint16_t* d = base + (long long)(th >> 4) * g.F + e;
+#pragma unroll
+    for (int q = 0; q < kChunk / 8; ++q) {
+      if ((th >> 4) + q * 8 < rows) {
+        if (STORE)
+          *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+        else
+          *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(d);
+      }
+      s += 8 * kPitch;
+      d += 8LL * g.F;
+    }
+    return;
+  }
+  constexpr int kVecs = kLanes / 8 + 1;
+  for (int i = th; i < rows * kVecs; i += 128) {
+    const int r = i / kVecs;
+    uint16_t* row = base + (long long)r * g.F;
+    const int shift = (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
+    const int e = (i - r * kVecs) * 8 - shift;  // first entry of the vector, counted in the row
+    uint16_t* s = stage + r * kPitch;
+    if (e >= 0 && e + 8 <= nf) {
+      if (STORE) {
+        // entries e .. e + 7 lie across five 4-byte words when e is odd (the word
+        // past the row's end is its padding)
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(s) + (e >> 1);
+        const uint32_t sh = (e & 1) * 16;
+        uint32_t a[5];
+#pragma unroll
+        for (int q = 0; q < 5; ++q) a[q] = w[q];
+        *reinterpret_cast<uint4*>(row + e) =
+            make_uint4(__funnelshift_r(a[0], a[1], sh), __funnelshift_r(a[1], a[2], sh), __funnelshift_r(a[2], a[3], sh),
+                       __funnelshift_r(a[3], a[4], sh));
+      } else {
+        alignas(16) uint16_t a[8];
+        *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(row + e);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[e + q] = a[q];
+      }
+    } else {
+      for (int q = max(e, 0); q < min(e + 8, nf); ++q) {
+        if (STORE)
+          row[q] = s[q];
+        else
+          s[q] = row[q];
+      }
+    }
+  }
 }
 
 // ORs a flag over the epilogue's threads (and is their barrier).
@@ -300,12 +362,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int fl = rank * kLanes + quarter * 32 + lane;  // lane of the tile
+    const int th = tid - 64 - half * 128;  // thread of the half
+    const int ln = quarter * 32 + lane;    // lane of this CTA's part of the tile
     const uint32_t acc_free[2] = {map_rank(su32(&acc_empty[0]), 0), map_rank(su32(&acc_empty[1]), 0)};
+    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kOffStage) + half * kChunk * kPitch;
+    const uint32_t mat = su32(stage) + ((lane & 7) * kPitch + quarter * 32 + (lane >> 3) * 8) * 2;
+    float* scales = reinterpret_cast<float*>(smem + kOffScale);
+    // the features whose values this thread holds: one lane's, or four rows of its fragments
+    const int nrow = g.staged ? 4 : 1, row0 = g.staged ? quarter * 32 + (lane >> 2) : ln;
+    float ls[4], bias[4];
+
+    // 32 columns from c of the tile to the outputs
+    auto finish = [&](float* v, int f0, int t0, int c, const float* cs) {
+      if (!g.staged) {
+        if (g.lane_scale) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= ls[0] * cs[c + j];
+        }
+        if (g.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += bias[0];
+        }
+        direct32(g, v, f0 + ln, t0 + c, min(kChunk, g.nt - c));
+        return;
+      }
+      if (g.lane_scale) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 s = *reinterpret_cast<const float2*>(cs + c + 8 * k + 2 * (lane & 3));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[16 * (i >> 1) + 4 * k + 2 * (i & 1)] *= ls[i] * s.x;
+            v[16 * (i >> 1) + 4 * k + 2 * (i & 1) + 1] *= ls[i] * s.y;
+          }
+        }
+      }
+      if (g.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += bias[2 * (j >> 4) + ((j >> 1) & 1)];
+      }
+      const int rows = min(min(kChunk, g.nt - c), g.T - t0 - c), nf = min(kLanes, g.F - f0);
+      auto put = [&](void* p) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+            w[i] = pack_bf16x2(a[0], a[1]);
+          }
+          store_matrix_t(mat + k * 8 * kPitch * 2, w);
+        }
+        half_bar(half);
+        move_rows<true>(g, stage, p, f0, nf, t0 + c, rows, th);
+        half_bar(half);  // the stage is free again
+      };
+      if (g.pre) put(g.pre);
+      activate32(v, g.act);
+      if (g.residual) {
+        move_rows<false>(g, stage, const_cast<void*>(g.residual), f0, nf, t0 + c, rows, th);
+        half_bar(half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+          load_matrix_t(mat + k * 8 * kPitch * 2, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+            a[0] += __uint_as_float(w[i] << 16);
+            a[1] += __uint_as_float(w[i] & 0xffff0000u);
+          }
+        }
+      }
+      put(g.out);
+    };
+
     int ti = 0;
     for (int u = pair; u < units; u += pairs, ++ti) {
       const int buf = ti & 1, tile = u / g.splits, sp = u % g.splits;
-      const int f = tile / g.tiles_t * kTileF + fl, t0 = tile % g.tiles_t * g.nt;
+      const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt;
+      float* cs = scales + buf * kMaxCols;  // a half is at most one unit ahead of the other
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int f = f0 + row0 + 8 * i;
+        const bool in = i < nrow && f < g.F;
+        ls[i] = g.lane_scale && in ? __ldg(g.lane_scale + f) : 0.f;
+        bias[i] = g.bias && in ? __ldg(g.bias + f) : 0.f;
+      }
+      if (g.col_scale) cs[tid - 64] = t0 + tid - 64 < g.T ? __ldg(g.col_scale + t0 + tid - 64) : 0.f;
       const bool ok = !*dead && mbar_wait_bounded(su32(&acc_full[buf]), (ti >> 1) & 1);
       if (epi_any(!ok)) {
         if (tid == 64 && !*dead) report_wait(g.status, kWhereAccFull, 0);
@@ -314,37 +458,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
-      float* part = g.splits > 1 ? g.partial + (size_t)tile * g.splits * g.nt * kTileF : nullptr;
-      for (int c = half * 16; c < g.nt; c += 32) {
-        if (t0 + c >= g.T) break;
-        float v[16];
-        tmem_ld16(src + c, v);
-        if (!part) {
-          finish16(g, v, f, t0 + c);
+      // partial sums in the threads' own order: [tile, split, CTA, chunk, value, thread of the half]
+      const int chunks = (g.nt + kChunk - 1) / kChunk;
+      float* part = g.partial + ((size_t)tile * g.splits * 2 + rank) * chunks * (kChunk * 128) + th;
+      const size_t part_split = (size_t)2 * chunks * (kChunk * 128);
+      for (int c = half * kChunk; c < g.nt && t0 + c < g.T; c += 2 * kChunk) {
+        float v[32];
+        if (g.staged)
+          tmem_ld_frags(src + c, v);
+        else
+          tmem_ld_lanes(src + c, v);
+        if (g.splits == 1) {
+          finish(v, f0, t0, c, cs);
         } else {
+          float* p = part + sp * part_split + (size_t)(c / kChunk) * (kChunk * 128);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[((size_t)sp * g.nt + c + j) * kTileF + fl] = v[j];
+          for (int j = 0; j < 32; ++j) p[j * 128] = v[j];
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_free[buf]);
-      if (part) {
+      if (g.splits > 1) {
         __threadfence();
         epi_any(false);
         if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * tile + rank], 1u) == (unsigned)g.splits - 1;
         epi_any(false);
         if (*(volatile int*)last_flag) {
           __threadfence();
-          for (int c = half * 16; c < g.nt; c += 32) {
-            if (t0 + c >= g.T) break;
-            float v[16];
+          for (int c = half * kChunk; c < g.nt && t0 + c < g.T; c += 2 * kChunk) {
+            const float* p = part + (size_t)(c / kChunk) * (kChunk * 128);
+            float v[32];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.f;
-            for (int q = 0; q < g.splits; ++q)
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int q = 0; q < g.splits; ++q, p += part_split)
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] += __ldcg(&part[((size_t)q * g.nt + c + j) * kTileF + fl]);
-            finish16(g, v, f, t0 + c);
+              for (int j = 0; j < 32; ++j) v[j] += __ldcg(p + j * 128);
+            finish(v, f0, t0, c, cs);
           }
         }
       }
@@ -408,7 +558,7 @@ __global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* p
 struct Plan {
   int nt, tiles_f, tiles_t, splits;
   size_t partial_bytes() const {
-    return splits > 1 ? (size_t)tiles_f * tiles_t * splits * nt * kTileF * sizeof(float) : 0;
+    return splits > 1 ? (size_t)tiles_f * tiles_t * splits * round_up(nt, kChunk) * kTileF * sizeof(float) : 0;
   }
   size_t counter_bytes() const { return splits > 1 ? round_up((size_t)tiles_f * tiles_t * 2 * sizeof(unsigned int), 256) : 0; }
   size_t bytes() const { return counter_bytes() + round_up(partial_bytes(), 256); }
@@ -463,6 +613,9 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
   g.tiles_f = p.tiles_f;
   g.tiles_t = p.tiles_t;
   g.splits = p.splits;
+  const auto align = [](const void* q) { return reinterpret_cast<uintptr_t>(q) & 15u; };
+  g.staged = g.out_type == DSPARK_BF16 && (!g.residual || align(g.residual) == align(g.out)) &&
+             (!g.pre || align(g.pre) == align(g.out));
   cudaError_t e;
   if (p.splits > 1) {
     g.counter = reinterpret_cast<unsigned int*>(scratch);

@@ -73,17 +73,57 @@ __device__ __forceinline__ void mma_commit(uint64_t* b) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// 16 accumulator columns of this warp's 32 lanes
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
+#define DSPARK_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+
+// 32 accumulator columns of this warp's 32 lanes: v[j] is column j of lane `lane`.
+__device__ __forceinline__ void tmem_ld_lanes(uint32_t taddr, float* v) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : DSPARK_R8(r, 0), DSPARK_R8(r, 8), DSPARK_R8(r, 16), DSPARK_R8(r, 24)
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same 32 x 32 block as 8 x 8 matrix fragments: v[16 h + 4 k + 2 i + e] is
+// lane 16 h + 8 i + lane / 4, column 8 k + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : DSPARK_R8(r, 16 * h), DSPARK_R8(r, 16 * h + 8)
+        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+#undef DSPARK_R8
+
+// Four 8 x 8 matrices of 16-bit entries, transposed between registers (as above,
+// two columns a register) and shared memory (a row of 8 lanes per column);
+// thread t gives the address of row t % 8 of matrix t / 8.
+__device__ __forceinline__ void store_matrix_t(uint32_t addr, const uint32_t* p) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[0]), "r"(p[1]),
+               "r"(p[2]), "r"(p[3])
+               : "memory");
+}
+__device__ __forceinline__ void load_matrix_t(uint32_t addr, uint32_t* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two fp32 values rounded to nearest-even bf16, packed (lo in the low half).
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // ---------------------------------------------------------------------------

@@ -97,6 +97,31 @@ def test_wide_outputs_and_many_tiles(cuda_ok):
     run(600, 20000, 192, seed=6, bias=True)
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 264, 64), (33, 517, 2048), (300, 1001, 128)])
+@pytest.mark.parametrize("offs", [(0, 0, 0), (1, 1, 1), (3, 3, 0), (0, 5, 0), (0, 0, 1), (7, 0, 2)])
+def test_outputs_of_any_alignment(cuda_ok, M, N, K, offs):
+    """y, residual and pre start at any 2-byte boundary, alike or not."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, _ = operand(M, K, False, g)
+    w, _ = operand(N, K, False, g, K ** -0.5)
+    r = torch.randn(M, N, generator=g, device="cuda").to(BF16)
+    want, wpre = torch.empty(M, N, device="cuda", dtype=BF16), torch.empty(M, N, device="cuda", dtype=BF16)
+    bn.linear(x, w, want, workspace(M, N, K), residual=r, pre=wpre, act="gelu")
+
+    def at(off):
+        flat = torch.full((M * N + 16,), 7.0, device="cuda", dtype=BF16)
+        return flat, flat[off:off + M * N].view(M, N)
+
+    (fy, y), (_, rr), (fp, p) = at(offs[0]), at(offs[1]), at(offs[2])
+    rr.copy_(r)
+    bn.linear(x, w, y, workspace(M, N, K), residual=rr, pre=p, act="gelu")
+    assert torch.equal(y, want) and torch.equal(p, wpre)
+    for flat, off in ((fy, offs[0]), (fp, offs[2])):
+        assert bool((flat[:off] == 7).all() and (flat[off + M * N:] == 7).all())
+    bn.linear(x, w, rr, workspace(M, N, K), residual=rr, act="gelu")
+    assert torch.equal(rr, want)
+
+
 def test_split_contraction_is_deterministic(cuda_ok):
     a = run(8, 200, 8192, seed=7, bias=True, act="silu")
     for _ in range(5):
