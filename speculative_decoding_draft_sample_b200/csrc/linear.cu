@@ -21,9 +21,9 @@
 //              of stages; the bytes of both CTAs complete on the first one's barrier
 //   warp 1     tensor-memory allocation and, in the first CTA, the single-thread
 //              tcgen05.mma issuer
-//   warps 2-9  epilogue of the previous unit meanwhile (two accumulators): a warp
-//              reads its quarter of the lanes (hardware: warp index mod 4), the two
-//              halves take alternate blocks of 16 columns
+//   warps 2-17 epilogue of the previous unit meanwhile (two accumulators): a warp
+//              reads its quarter of the lanes (hardware: warp index mod 4), the four
+//              warps of a quarter take blocks of 32 columns in turn
 // With fewer tiles than pairs the contraction is split: each part leaves its fp32
 // sums in the workspace and the last to arrive adds them in order of the parts
 // (the result does not depend on who that is) and finishes the tile.
@@ -39,8 +39,9 @@ namespace {
 
 using namespace t5;
 
-constexpr int kThreads = 320;
-constexpr int kEpiThreads = 256;
+constexpr int kEpiWarps = 16;                  // four per quarter of the lanes, so that the latencies of a chunk overlap
+constexpr int kEpiThreads = 32 * kEpiWarps;
+constexpr int kThreads = 64 + kEpiThreads;
 constexpr int kTileF = 256;                    // lanes: output features per tile, 128 in each CTA of the pair
 constexpr int kLanes = 128;
 constexpr int kMaxCols = 256;                  // columns per tile at most
@@ -48,10 +49,10 @@ constexpr int kABytes = kLanes * 128;          // A of a stage: 128 bytes of con
 constexpr int kMaxStages = 12;
 constexpr int kRing = 6 * 32768;               // bytes of the stage ring
 constexpr int kBoxBytes = 64 * 128;            // one [64 x 128 bytes] box of a lane- or column-contiguous operand
-constexpr int kChunk = 32;                     // columns that one half of the epilogue takes at a time
-constexpr int kPitch = kLanes + 8;             // entries of a staged row: 8 rows of 16 bytes fall on all banks
+constexpr int kChunk = 32;                     // columns that an epilogue warp takes at a time
+constexpr int kStageBytes = kChunk * 64;       // a warp's staged chunk: 32 columns x 32 lanes of 2 bytes
 constexpr int kOffStage = kRing;
-constexpr int kOffScale = kOffStage + 2 * kChunk * kPitch * 2;  // col_scale of the tile, two buffers
+constexpr int kOffScale = kOffStage + kEpiWarps * kStageBytes;  // col_scale of the tile, two buffers
 constexpr int kOffBar = kOffScale + 2 * kMaxCols * 4;
 constexpr int kNumBars = 2 * kMaxStages + 4;
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
@@ -77,7 +78,7 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  int staged;               // bf16 outputs, aligned alike: through shared memory
+  int staged;               // bf16 rows of whole 16-byte vectors: through shared memory
   float* partial;           // [tile, split, 2, nt rounded up to 32, 128] (splits > 1)
   unsigned int* counter;    // [tile, CTA of the pair], zero at launch (splits > 1)
   Status* status;
@@ -124,7 +125,7 @@ __device__ __forceinline__ void activate32(float* v, int act) {
   }
 }
 
-// fp32 outputs (and 2-byte tensors that are not aligned alike): one lane's
+// fp32 outputs (and 2-byte rows that are not whole 16-byte vectors): one lane's
 // columns straight to memory, 32 neighbouring outputs per warp and store. All
 // loads come before the first store: a load behind a store that might alias it
 // waits for its turn.
@@ -150,68 +151,30 @@ __device__ __forceinline__ void direct32(const Gemm& g, float* v, int f, int t0,
     if (j < n) store_out(g.out, at + (long long)j * g.F, g.out_type, v[j]);
 }
 
-__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory"); }
+// bf16 outputs whose rows are whole 16-byte vectors go through shared memory: a
+// lane holds features of many tokens, memory wants many features of one token.
+// A warp's stage is its own (no barrier but the warp's): row r is token t0 + r,
+// 32 features in four 16-byte vectors, vector q at q ^ (r / 2 % 4), so that eight
+// rows of one vector and two rows of four both fall on all banks.
+__device__ __forceinline__ uint32_t stage_at(int r, int q) { return r * 64 + ((q ^ ((r >> 1) & 3)) << 4); }
 
-// bf16 outputs go through shared memory: a lane holds one feature of many
-// tokens, memory wants many features of one token. Row j of the stage holds the
-// 128 features of token t0 + j. Between stage and memory rows move as 16-byte
-// vectors of the memory's alignment: 16 of them where the width is a multiple of
-// 8 entries, else (any width, any 2-byte alignment) up to 17, the vectors inside
-// the row read from the stage at their odd offset, up to 7 entries singly at
-// either end. `rows` tokens from t0, features f0 .. f0 + nf - 1; 128 threads (th).
+// Moves rows between a warp's stage and memory (p: token t0, the warp's first
+// feature; nf features of the row remain): 8 rows x 64 bytes an instruction.
 template <bool STORE>
-__device__ __forceinline__ void move_rows(const Gemm& g, uint16_t* stage, void* p, int f0, int nf, int t0, int rows, int th) {
-  uint16_t* base = static_cast<uint16_t*>(p) + (long long)t0 * g.F + f0;
-  if ((g.F & 7) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    const int e = (th & 15) * 8;
-    if (e >= nf) return;
-    uint16_t* s = stage + (th >> 4) * kPitch + e;
-    uint16_t* d = base + (long long)(th >> 4) * g.F + e;
+__device__ __forceinline__ void move_rows(unsigned char* stage, uint16_t* p, int F, int nf, int rows, int lane) {
+  const int q = lane & 3;
+  if (q * 8 >= nf) return;
+  p += (long long)(lane >> 2) * F + q * 8;
 #pragma unroll
-    for (int q = 0; q < kChunk / 8; ++q) {
-      if ((th >> 4) + q * 8 < rows) {
-        if (STORE)
-          *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
-        else
-          *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(d);
-      }
-      s += 8 * kPitch;
-      d += 8LL * g.F;
-    }
-    return;
-  }
-  constexpr int kVecs = kLanes / 8 + 1;
-  for (int i = th; i < rows * kVecs; i += 128) {
-    const int r = i / kVecs;
-    uint16_t* row = base + (long long)r * g.F;
-    const int shift = (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
-    const int e = (i - r * kVecs) * 8 - shift;  // first entry of the vector, counted in the row
-    uint16_t* s = stage + r * kPitch;
-    if (e >= 0 && e + 8 <= nf) {
-      if (STORE) {
-        // entries e .. e + 7 lie across five 4-byte words when e is odd (the word
-        // past the row's end is its padding)
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(s) + (e >> 1);
-        const uint32_t sh = (e & 1) * 16;
-        uint32_t a[5];
-#pragma unroll
-        for (int q = 0; q < 5; ++q) a[q] = w[q];
-        *reinterpret_cast<uint4*>(row + e) =
-            make_uint4(__funnelshift_r(a[0], a[1], sh), __funnelshift_r(a[1], a[2], sh), __funnelshift_r(a[2], a[3], sh),
-                       __funnelshift_r(a[3], a[4], sh));
-      } else {
-        alignas(16) uint16_t a[8];
-        *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(row + e);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s[e + q] = a[q];
-      }
-    } else {
-      for (int q = max(e, 0); q < min(e + 8, nf); ++q) {
-        if (STORE)
-          row[q] = s[q];
-        else
-          s[q] = row[q];
-      }
+  for (int i = 0; i < kChunk / 8; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (r < rows) {
+      uint4* s = reinterpret_cast<uint4*>(stage + stage_at(r, q));
+      uint4* d = reinterpret_cast<uint4*>(p + (long long)(i * 8) * F);
+      if (STORE)
+        *d = *s;
+      else
+        *s = *d;
     }
   }
 }
@@ -220,7 +183,7 @@ __device__ __forceinline__ void move_rows(const Gemm& g, uint16_t* stage, void* 
 __device__ __forceinline__ bool epi_any(bool flag) {
   uint32_t r;
   asm volatile(
-      "{ .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{ .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
       : "r"((uint32_t)flag)
       : "memory");
@@ -281,25 +244,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The producer and the issuer are one thread each, whose loop has to keep up
+  // with a block of 512 tensor-core cycles: stages and phases are counted, not
+  // divided, and addresses and descriptors advance by additions (a loop that
+  // computed them anew took 730 cycles a block).
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0, last = -1;
+      const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
       for (int u = pair; u < units && !*dead; u += pairs) {
         const int tile = u / g.splits;
         const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt + rank * nh;
         int k0, k1;
         blocks(u, k0, k1);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int s = it % stages;
-          if (!mbar_wait_bounded(su32(&empty[s]), ((it / stages) & 1) ^ 1)) {
+        int kx = k0 * (F8 ? 128 : 64);
+        for (int kb = k0; kb < k1; ++kb, kx += F8 ? 128 : 64) {
+          if (!mbar_wait(&empty[s], ph)) {
             if (!*dead) report_wait(g.status, kWhereEmpty, 0);
             *dead = 1;
             break;
           }
           if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
-          const uint32_t bar = map_rank(su32(&full[s]), 0);
-          const uint32_t a = su32(smem) + s * stage_bytes, b = a + kABytes;
-          const int kx = kb * (F8 ? 128 : 64);
+          const uint32_t bar = full0 + 8 * s;
+          const uint32_t a = smem0 + s * stage_bytes, b = a + kABytes;
           if (A_MN) {
             tma_load_2d(a, &map_a, f0, kx, bar);
             tma_load_2d(a + kBoxBytes, &map_a, f0 + 64, kx, bar);
@@ -311,12 +279,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d(b, &map_b, kx, t0, bar);
           }
-          last = it;
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
       if (*dead && rank == 0)  // let issued loads of both CTAs land before the pair winds down (below)
-        for (int q = max(0, last - stages + 1); q <= last; ++q)
-          mbar_wait_bounded(su32(&full[q % stages]), (q / stages) & 1);
+        for (int q = max(0, issued - stages); q < issued; ++q) mbar_wait(&full[q % stages], (q / stages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -324,10 +295,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // D fp32; A and B bf16 or e4m3; widths nt and 256
       const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) |
                              ((uint32_t)B_MN << 16) | ((uint32_t)(g.nt >> 3) << 17) | ((uint32_t)(kTileF >> 4) << 24);
-      int it = 0, ti = 0;
-      for (int u = pair; u < units && !*dead; u += pairs, ++ti) {
-        const int buf = ti & 1;
-        if (!mbar_wait_bounded(su32(&acc_empty[buf]), ((ti >> 1) & 1) ^ 1)) {
+      // descriptors of the first stage; their low bits are the address in 16-byte units
+      const uint64_t desc_a = A_MN ? sdesc(su32(smem), kBoxBytes, 1024) : sdesc(su32(smem), 16, 1024);
+      const uint64_t desc_b = B_MN ? sdesc(su32(smem) + kABytes, kBoxBytes, 1024) : sdesc(su32(smem) + kABytes, 16, 1024);
+      constexpr uint64_t step_a = (A_MN ? 2048 : 32) >> 4, step_b = (B_MN ? 2048 : 32) >> 4;
+      int s = 0, done = 0;
+      uint32_t ph = 0, aph = 1, buf = 0;
+      uint64_t da = desc_a, db = desc_b;
+      for (int u = pair; u < units && !*dead; u += pairs) {
+        if (!mbar_wait(&acc_empty[buf], aph)) {
           if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
           *dead = 1;
           break;
@@ -336,37 +312,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int k0, k1;
         blocks(u, k0, k1);
         const uint32_t d = tmem + buf * kMaxCols;
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int s = it % stages;
-          if (!mbar_wait_bounded(su32(&full[s]), (it / stages) & 1)) {
+        uint32_t acc = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(&full[s], ph)) {
             if (!*dead) report_wait(g.status, kWhereFull, 0);
             *dead = 1;
             break;
           }
           fence_after();
-          const uint32_t a = su32(smem) + s * stage_bytes, b = a + kABytes;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {  // 32 bytes of the contraction (or 16 rows of it) each
-            const uint64_t ad = A_MN ? sdesc(a + q * 2048, kBoxBytes, 1024) : sdesc(a + q * 32, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc(b + q * 2048, kBoxBytes, 1024) : sdesc(b + q * 32, 16, 1024);
-            mma<F8>(d, ad, bd, idesc, kb > k0 || q > 0);
+            mma<F8>(d, da + q * step_a, db + q * step_b, idesc, acc);
+            acc = 1;
           }
           mma_commit(&empty[s]);
+          ++done;
+          da += stage_bytes >> 4;
+          db += stage_bytes >> 4;
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+            da = desc_a;
+            db = desc_b;
+          }
         }
         if (*dead) break;
         mma_commit(&acc_full[buf]);
+        buf ^= 1;
+        if (buf == 0) aph ^= 1;
       }
-      if (*dead && it > 0)  // MMAs complete in order: after the last commit tensor memory is quiet
-        mbar_wait_bounded(su32(&empty[(it - 1) % stages]), ((it - 1) / stages) & 1);
+      if (*dead && done > 0)  // MMAs complete in order: after the last commit tensor memory is quiet
+        mbar_wait(&empty[(done - 1) % stages], ((done - 1) / stages) & 1);
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int th = tid - 64 - half * 128;  // thread of the half
+    const int quarter = warp & 3, group = (warp - 2) >> 2, th = tid - 64;
     const int ln = quarter * 32 + lane;    // lane of this CTA's part of the tile
     const uint32_t acc_free[2] = {map_rank(su32(&acc_empty[0]), 0), map_rank(su32(&acc_empty[1]), 0)};
-    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + kOffStage) + half * kChunk * kPitch;
-    const uint32_t mat = su32(stage) + ((lane & 7) * kPitch + quarter * 32 + (lane >> 3) * 8) * 2;
+    unsigned char* stage = smem + kOffStage + (warp - 2) * kStageBytes;
+    const uint32_t mat = su32(stage) + stage_at(lane & 7, lane >> 3);  // + 512 for the next 8 columns
     float* scales = reinterpret_cast<float*>(smem + kOffScale);
     // the features whose values this thread holds: one lane's, or four rows of its fragments
     const int nrow = g.staged ? 4 : 1, row0 = g.staged ? quarter * 32 + (lane >> 2) : ln;
@@ -401,7 +385,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += bias[2 * (j >> 4) + ((j >> 1) & 1)];
       }
-      const int rows = min(min(kChunk, g.nt - c), g.T - t0 - c), nf = min(kLanes, g.F - f0);
+      const int rows = min(min(kChunk, g.nt - c), g.T - t0 - c), fw = f0 + quarter * 32;
+      const long long at = (long long)(t0 + c) * g.F + fw;
       auto put = [&](void* p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -411,21 +396,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
             w[i] = pack_bf16x2(a[0], a[1]);
           }
-          store_matrix_t(mat + k * 8 * kPitch * 2, w);
+          store_matrix_t(mat + k * 512, w);
         }
-        half_bar(half);
-        move_rows<true>(g, stage, p, f0, nf, t0 + c, rows, th);
-        half_bar(half);  // the stage is free again
+        __syncwarp();
+        move_rows<true>(stage, static_cast<uint16_t*>(p) + at, g.F, g.F - fw, rows, lane);
+        __syncwarp();  // the stage is free again
       };
       if (g.pre) put(g.pre);
       activate32(v, g.act);
       if (g.residual) {
-        move_rows<false>(g, stage, const_cast<void*>(g.residual), f0, nf, t0 + c, rows, th);
-        half_bar(half);
+        move_rows<false>(stage, const_cast<uint16_t*>(static_cast<const uint16_t*>(g.residual)) + at, g.F, g.F - fw, rows, lane);
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t w[4];
-          load_matrix_t(mat + k * 8 * kPitch * 2, w);
+          load_matrix_t(mat + k * 512, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
@@ -433,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             a[1] += __uint_as_float(w[i] & 0xffff0000u);
           }
         }
+        __syncwarp();
       }
       put(g.out);
     };
@@ -441,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = pair; u < units; u += pairs, ++ti) {
       const int buf = ti & 1, tile = u / g.splits, sp = u % g.splits;
       const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt;
-      float* cs = scales + buf * kMaxCols;  // a half is at most one unit ahead of the other
+      float* cs = scales + buf * kMaxCols;  // no warp is more than one unit ahead of another
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int f = f0 + row0 + 8 * i;
@@ -449,8 +435,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ls[i] = g.lane_scale && in ? __ldg(g.lane_scale + f) : 0.f;
         bias[i] = g.bias && in ? __ldg(g.bias + f) : 0.f;
       }
-      if (g.col_scale) cs[tid - 64] = t0 + tid - 64 < g.T ? __ldg(g.col_scale + t0 + tid - 64) : 0.f;
-      const bool ok = !*dead && mbar_wait_bounded(su32(&acc_full[buf]), (ti >> 1) & 1);
+      if (g.col_scale && th < kMaxCols) cs[th] = t0 + th < g.T ? __ldg(g.col_scale + t0 + th) : 0.f;
+      const bool ok = !*dead && mbar_wait(&acc_full[buf], (ti >> 1) & 1);
       if (epi_any(!ok)) {
         if (tid == 64 && !*dead) report_wait(g.status, kWhereAccFull, 0);
         *dead = 1;
@@ -458,11 +444,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
-      // partial sums in the threads' own order: [tile, split, CTA, chunk, value, thread of the half]
+      // partial sums in the threads' own order: [tile, split, CTA, chunk, value, lane]
       const int chunks = (g.nt + kChunk - 1) / kChunk;
-      float* part = g.partial + ((size_t)tile * g.splits * 2 + rank) * chunks * (kChunk * 128) + th;
+      float* part = g.partial + ((size_t)tile * g.splits * 2 + rank) * chunks * (kChunk * 128) + ln;
       const size_t part_split = (size_t)2 * chunks * (kChunk * 128);
-      for (int c = half * kChunk; c < g.nt && t0 + c < g.T; c += 2 * kChunk) {
+      for (int c = group * kChunk; c < g.nt && t0 + c < g.T; c += kEpiWarps / 4 * kChunk) {
         float v[32];
         if (g.staged)
           tmem_ld_frags(src + c, v);
@@ -486,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         epi_any(false);
         if (*(volatile int*)last_flag) {
           __threadfence();
-          for (int c = half * kChunk; c < g.nt && t0 + c < g.T; c += 2 * kChunk) {
+          for (int c = group * kChunk; c < g.nt && t0 + c < g.T; c += kEpiWarps / 4 * kChunk) {
             const float* p = part + (size_t)(c / kChunk) * (kChunk * 128);
             float v[32];
 #pragma unroll
@@ -613,9 +599,7 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
   g.tiles_f = p.tiles_f;
   g.tiles_t = p.tiles_t;
   g.splits = p.splits;
-  const auto align = [](const void* q) { return reinterpret_cast<uintptr_t>(q) & 15u; };
-  g.staged = g.out_type == DSPARK_BF16 && (!g.residual || align(g.residual) == align(g.out)) &&
-             (!g.pre || align(g.pre) == align(g.out));
+  g.staged = g.out_type == DSPARK_BF16 && g.F % 8 == 0 && aligned16(g.out) && aligned16(g.residual) && aligned16(g.pre);
   cudaError_t e;
   if (p.splits > 1) {
     g.counter = reinterpret_cast<unsigned int*>(scratch);

@@ -22,6 +22,28 @@ __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
 }
+// Bounded wait for the phase of parity `par`; false when it gave up (kWaitLimitNs).
+// The timer is read only once polling has lasted a while: its first read would
+// cost more than most waits here last.
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t par) {
+  const uint32_t bar = su32(b);
+  unsigned long long start = 0;
+  for (unsigned it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(par)
+        : "memory");
+    if (ok) return true;
+    if ((it & 255u) == 0) {
+      const unsigned long long now = global_ns();
+      if (start == 0) start = now;
+      else if (now - start > kWaitLimitNs) return false;
+    }
+  }
+}
+
 // Pair of CTAs (cta_group::2): one issues the matrix instructions for both.
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
