@@ -52,8 +52,7 @@ constexpr int kBoxBytes = 64 * 128;            // one [64 x 128 bytes] box of a 
 constexpr int kChunk = 32;                     // columns that an epilogue warp takes at a time
 constexpr int kStageBytes = kChunk * 64;       // a warp's staged chunk: 32 columns x 32 lanes of 2 bytes
 constexpr int kOffStage = kRing;
-constexpr int kOffScale = kOffStage + kEpiWarps * kStageBytes;  // col_scale of the tile, two buffers
-constexpr int kOffBar = kOffScale + 2 * kMaxCols * 4;
+constexpr int kOffBar = kOffStage + kEpiWarps * kStageBytes;
 constexpr int kNumBars = 2 * kMaxStages + 4;
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
 static_assert(kSmem <= 232448, "exceeds the 227 KB of shared memory per block");
@@ -89,15 +88,6 @@ __device__ __forceinline__ float gate(float z, float v) { return __fdividef(z, 1
 
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case DSPARK_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
-    case DSPARK_ACT_SILU: return gate(z, z);
-    case DSPARK_ACT_GELU: return gate(z, kGelu2 * fmaf(0.044715f * z * z, z, z));
-    default: return z;
-  }
-}
-
 // act'(z); past |z| = 64 both gates are 0 or 1 exactly
 __device__ __forceinline__ float activate_grad(float z, int act) {
   if (act == DSPARK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
@@ -108,47 +98,47 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
   return g + z * g * (1.f - g) * dv;
 }
 
-__device__ __forceinline__ float load_out(const void* p, long long i, int type) {
-  return type == DSPARK_F32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
-}
-__device__ __forceinline__ void store_out(void* p, long long i, int type, float v) {
-  if (type == DSPARK_F32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<uint16_t*>(p)[i] = Elem<DSPARK_BF16>::store_round(v);
-}
-
 __device__ __forceinline__ void activate32(float* v, int act) {
-  if (act != DSPARK_ACT_NONE) {
+  if (act == DSPARK_ACT_RELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], act);
+    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];  // NaN stays
+  } else if (act == DSPARK_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = gate(v[j], v[j]);
+  } else if (act == DSPARK_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = gate(v[j], kGelu2 * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
   }
 }
 
 // fp32 outputs (and 2-byte rows that are not whole 16-byte vectors): one lane's
 // columns straight to memory, 32 neighbouring outputs per warp and store. All
 // loads come before the first store: a load behind a store that might alias it
-// waits for its turn.
-__device__ __forceinline__ void direct32(const Gemm& g, float* v, int f, int t0, int cols) {
-  if (f >= g.F) return;
-  const int n = min(cols, g.T - t0);
-  const long long at = (long long)t0 * g.F + f;
+// waits for its turn. at: column 0; n columns.
+template <int DT>
+__device__ __forceinline__ void direct32(const Gemm& g, float* v, long long at, int n) {
+  using T = typename Elem<DT>::T;
   if (g.pre) {
+    T* p = static_cast<T*>(g.pre) + at;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) store_out(g.pre, at + (long long)j * g.F, g.out_type, v[j]);
+    for (int j = 0; j < 32; ++j, p += g.F)
+      if (j < n) *p = Elem<DT>::store_round(v[j]);
   }
   activate32(v, g.act);
   if (g.residual) {
-    float res[32];
+    const T* p = static_cast<const T*>(g.residual) + at;
+    T res[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) res[j] = j < n ? load_out(g.residual, at + (long long)j * g.F, g.out_type) : 0.f;
+    for (int j = 0; j < 32; ++j, p += g.F)
+      if (j < n) res[j] = *p;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += res[j];
+    for (int j = 0; j < 32; ++j)
+      if (j < n) v[j] += Elem<DT>::to_float(res[j]);
   }
+  T* p = static_cast<T*>(g.out) + at;
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < n) store_out(g.out, at + (long long)j * g.F, g.out_type, v[j]);
+  for (int j = 0; j < 32; ++j, p += g.F)
+    if (j < n) *p = Elem<DT>::store_round(v[j]);
 }
 
 // bf16 outputs whose rows are whole 16-byte vectors go through shared memory: a
@@ -179,16 +169,50 @@ __device__ __forceinline__ void move_rows(unsigned char* stage, uint16_t* p, int
   }
 }
 
-// ORs a flag over the epilogue's threads (and is their barrier).
-__device__ __forceinline__ bool epi_any(bool flag) {
-  uint32_t r;
-  asm volatile(
-      "{ .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)flag)
-      : "memory");
-  return r != 0;
-}
+// The work units of a pair, u = pair, pair + pairs, ...: unit u is part
+// u % splits of tile u / splits, and tiles run over the columns first, so that
+// pairs working at the same time share their rows of A. Steps by additions: a
+// unit of a short contraction lasts less than four divisions in a row.
+struct Units {
+  int u, left, sp, tt, tf;
+  int dsp, dtt, dtf, splits, tiles_t;
+  __device__ __forceinline__ Units(const Gemm& g, int pair, int pairs)
+      : u(pair), splits(g.splits), tiles_t(g.tiles_t) {
+    const int units = g.tiles_f * g.tiles_t * g.splits;
+    left = units > pair ? (units - pair + pairs - 1) / pairs : 0;
+    sp = pair % splits;
+    tt = pair / splits % tiles_t;
+    tf = pair / splits / tiles_t;
+    dsp = pairs % splits;
+    dtt = pairs / splits % tiles_t;
+    dtf = pairs / splits / tiles_t;
+  }
+  __device__ __forceinline__ void next() {
+    --left;
+    sp += dsp;
+    tt += dtt;
+    tf += dtf;
+    if (sp >= splits) {
+      sp -= splits;
+      ++tt;
+    }
+    if (tt >= tiles_t) {
+      tt -= tiles_t;
+      ++tf;
+    }
+  }
+  // the part's blocks of the contraction
+  __device__ __forceinline__ void blocks(const Gemm& g, int& k0, int& k1) const {
+    k0 = 0;
+    k1 = g.kblocks;
+    if (splits > 1) {
+      k0 = (int)((long long)g.kblocks * sp / splits);
+      k1 = (int)((long long)g.kblocks * (sp + 1) / splits);
+    }
+  }
+};
+
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 // A_MN / B_MN: the operand is contiguous along lanes / columns, not along the contraction.
 template <bool F8, bool A_MN, bool B_MN>
@@ -214,14 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int stage_bytes = kABytes + nh * 128;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int stages = min(kMaxStages, kRing / stage_bytes);
-  const int units = g.tiles_f * g.tiles_t * g.splits;
-  // unit u: part u % splits of tile u / splits; tiles run over the columns first,
-  // so that pairs working at the same time share their rows of A
-  auto blocks = [&](int u, int& k0, int& k1) {
-    const int sp = u % g.splits;
-    k0 = (int)((long long)g.kblocks * sp / g.splits);
-    k1 = (int)((long long)g.kblocks * (sp + 1) / g.splits);
-  };
+  Units w(g, pair, pairs);
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -253,11 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
       int s = 0, issued = 0;
       uint32_t ph = 1;
-      for (int u = pair; u < units && !*dead; u += pairs) {
-        const int tile = u / g.splits;
-        const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt + rank * nh;
+      for (; w.left > 0 && !*dead; w.next()) {
+        const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt + rank * nh;
         int k0, k1;
-        blocks(u, k0, k1);
+        w.blocks(g, k0, k1);
         int kx = k0 * (F8 ? 128 : 64);
         for (int kb = k0; kb < k1; ++kb, kx += F8 ? 128 : 64) {
           if (!mbar_wait(&empty[s], ph)) {
@@ -302,15 +318,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, done = 0;
       uint32_t ph = 0, aph = 1, buf = 0;
       uint64_t da = desc_a, db = desc_b;
-      for (int u = pair; u < units && !*dead; u += pairs) {
+      for (; w.left > 0 && !*dead; w.next()) {
+        int k0, k1;
+        w.blocks(g, k0, k1);
         if (!mbar_wait(&acc_empty[buf], aph)) {
           if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
           *dead = 1;
           break;
         }
         fence_after();
-        int k0, k1;
-        blocks(u, k0, k1);
         const uint32_t d = tmem + buf * kMaxCols;
         uint32_t acc = 0;
         for (int kb = k0; kb < k1; ++kb) {
@@ -346,38 +362,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, group = (warp - 2) >> 2, th = tid - 64;
+    const int quarter = warp & 3, group = (warp - 2) >> 2;
     const int ln = quarter * 32 + lane;    // lane of this CTA's part of the tile
-    const uint32_t acc_free[2] = {map_rank(su32(&acc_empty[0]), 0), map_rank(su32(&acc_empty[1]), 0)};
+    const uint32_t acc_free = map_rank(su32(acc_empty), 0);
     unsigned char* stage = smem + kOffStage + (warp - 2) * kStageBytes;
     const uint32_t mat = su32(stage) + stage_at(lane & 7, lane >> 3);  // + 512 for the next 8 columns
-    float* scales = reinterpret_cast<float*>(smem + kOffScale);
     // the features whose values this thread holds: one lane's, or four rows of its fragments
     const int nrow = g.staged ? 4 : 1, row0 = g.staged ? quarter * 32 + (lane >> 2) : ln;
     float ls[4], bias[4];
 
-    // 32 columns from c of the tile to the outputs
-    auto finish = [&](float* v, int f0, int t0, int c, const float* cs) {
+    // 32 columns from c of the tile to the outputs; cscale: lane j's is column j's scale
+    auto finish = [&](float* v, int f0, int t0, int c, float cscale) {
       if (!g.staged) {
         if (g.lane_scale) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= ls[0] * cs[c + j];
+          for (int j = 0; j < 32; ++j) v[j] *= ls[0] * __shfl_sync(0xffffffffu, cscale, j);
         }
         if (g.bias) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += bias[0];
         }
-        direct32(g, v, f0 + ln, t0 + c, min(kChunk, g.nt - c));
+        const int n = f0 + ln < g.F ? min(min(kChunk, g.nt - c), g.T - t0 - c) : 0;
+        const long long at = (long long)(t0 + c) * g.F + f0 + ln;
+        if (g.out_type == DSPARK_F32)
+          direct32<DSPARK_F32>(g, v, at, n);
+        else
+          direct32<DSPARK_BF16>(g, v, at, n);
         return;
       }
       if (g.lane_scale) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 s = *reinterpret_cast<const float2*>(cs + c + 8 * k + 2 * (lane & 3));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[16 * (i >> 1) + 4 * k + 2 * (i & 1)] *= ls[i] * s.x;
-            v[16 * (i >> 1) + 4 * k + 2 * (i & 1) + 1] *= ls[i] * s.y;
+          for (int e = 0; e < 2; ++e) {
+            const float s = __shfl_sync(0xffffffffu, cscale, 8 * k + 2 * (lane & 3) + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[16 * (i >> 1) + 4 * k + 2 * (i & 1) + e] *= ls[i] * s;
           }
         }
       }
@@ -423,11 +443,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       put(g.out);
     };
 
-    int ti = 0;
-    for (int u = pair; u < units; u += pairs, ++ti) {
-      const int buf = ti & 1, tile = u / g.splits, sp = u % g.splits;
-      const int f0 = tile / g.tiles_t * kTileF + rank * kLanes, t0 = tile % g.tiles_t * g.nt;
-      float* cs = scales + buf * kMaxCols;  // no warp is more than one unit ahead of another
+    // A warp whose wait gives up goes on without its work: the barriers of a
+    // split contraction expect every warp.
+    uint32_t buf = 0, aph = 0;
+    for (; w.left > 0; w.next()) {
+      const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int f = f0 + row0 + 8 * i;
@@ -435,44 +455,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ls[i] = g.lane_scale && in ? __ldg(g.lane_scale + f) : 0.f;
         bias[i] = g.bias && in ? __ldg(g.bias + f) : 0.f;
       }
-      if (g.col_scale && th < kMaxCols) cs[th] = t0 + th < g.T ? __ldg(g.col_scale + t0 + th) : 0.f;
-      const bool ok = !*dead && mbar_wait(&acc_full[buf], (ti >> 1) & 1);
-      if (epi_any(!ok)) {
-        if (tid == 64 && !*dead) report_wait(g.status, kWhereAccFull, 0);
+      bool ok = !*dead;
+      if (ok && !mbar_wait(&acc_full[buf], aph)) {
+        ok = false;
+        if (!*dead) report_wait(g.status, kWhereAccFull, 0);
         *dead = 1;
-        break;
       }
+      ok = __all_sync(0xffffffffu, ok);
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
       // partial sums in the threads' own order: [tile, split, CTA, chunk, value, lane]
-      const int chunks = (g.nt + kChunk - 1) / kChunk;
+      const int chunks = (g.nt + kChunk - 1) / kChunk, tile = w.tf * g.tiles_t + w.tt;
       float* part = g.partial + ((size_t)tile * g.splits * 2 + rank) * chunks * (kChunk * 128) + ln;
       const size_t part_split = (size_t)2 * chunks * (kChunk * 128);
-      for (int c = group * kChunk; c < g.nt && t0 + c < g.T; c += kEpiWarps / 4 * kChunk) {
+      const int c1 = ok ? min(g.nt, g.T - t0) : 0;
+      for (int c = group * kChunk; c < c1; c += kEpiWarps / 4 * kChunk) {
         float v[32];
+        const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
         if (g.staged)
           tmem_ld_frags(src + c, v);
         else
           tmem_ld_lanes(src + c, v);
+        if (c + kEpiWarps / 4 * kChunk >= c1) {  // the warp's last chunk: its part of the accumulator is free
+          fence_before();
+          if (lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);
+        }
         if (g.splits == 1) {
-          finish(v, f0, t0, c, cs);
+          finish(v, f0, t0, c, cscale);
         } else {
-          float* p = part + sp * part_split + (size_t)(c / kChunk) * (kChunk * 128);
+          float* p = part + w.sp * part_split + (size_t)(c / kChunk) * (kChunk * 128);
 #pragma unroll
           for (int j = 0; j < 32; ++j) p[j * 128] = v[j];
         }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_free[buf]);
+      if (group * kChunk >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
       if (g.splits > 1) {
         __threadfence();
-        epi_any(false);
+        epi_bar();
         if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * tile + rank], 1u) == (unsigned)g.splits - 1;
-        epi_any(false);
+        epi_bar();
         if (*(volatile int*)last_flag) {
           __threadfence();
-          for (int c = group * kChunk; c < g.nt && t0 + c < g.T; c += kEpiWarps / 4 * kChunk) {
+          for (int c = group * kChunk; c < c1; c += kEpiWarps / 4 * kChunk) {
+            const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
             const float* p = part + (size_t)(c / kChunk) * (kChunk * 128);
             float v[32];
 #pragma unroll
@@ -480,10 +505,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int q = 0; q < g.splits; ++q, p += part_split)
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] += __ldcg(p + j * 128);
-            finish(v, f0, t0, c, cs);
+            finish(v, f0, t0, c, cscale);
           }
         }
       }
+      buf ^= 1;
+      if (buf == 0) aph ^= 1;
     }
   }
   fence_before();
