@@ -143,8 +143,7 @@ int dspark_linear(const void* x, const void* w, const float* x_scale, const floa
   const uintptr_t es = out_type == DSPARK_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(pre) | reinterpret_cast<uintptr_t>(residual)) % es)
     return DSPARK_ERR_INVALID_ARG;
-  int sms = 0;
-  if (int e = ws_check(DSPARK_OP_LINEAR, M, 0, N, K, in_type, ws, ws_bytes, &sms)) return e;
+  if (int e = ws_check(DSPARK_OP_LINEAR, M, 0, N, K, in_type, ws, ws_bytes, nullptr)) return e;
   LinearArgs a;
   a.x = x;
   a.w = w;
@@ -162,7 +161,7 @@ int dspark_linear(const void* x, const void* w, const float* x_scale, const floa
   a.pre = pre;
   a.scratch = scratch_of(ws);
   a.status = static_cast<Status*>(ws);
-  return cuda_status(linear_launch(a, sms, (cudaStream_t)stream));
+  return cuda_status(linear_launch(a, (cudaStream_t)stream));
 }
 
 int dspark_linear_grad(const void* x, const void* w, const void* dy, const void* pre, int M, int N,
@@ -174,8 +173,7 @@ int dspark_linear_grad(const void* x, const void* w, const void* dy, const void*
   if (!linear_shape_ok(M, N, K, DSPARK_BF16) || N % 8 != 0) return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w) || !aligned16(dy) || !aligned16(pre) || !aligned16(dx) || !aligned16(dw))
     return DSPARK_ERR_INVALID_ARG;
-  int sms = 0;
-  if (int e = ws_check(DSPARK_OP_LINEAR, M, 0, N, K, DSPARK_BF16, ws, ws_bytes, &sms)) return e;
+  if (int e = ws_check(DSPARK_OP_LINEAR, M, 0, N, K, DSPARK_BF16, ws, ws_bytes, nullptr)) return e;
   LinearGradArgs a;
   a.x = x;
   a.w = w;
@@ -190,7 +188,7 @@ int dspark_linear_grad(const void* x, const void* w, const void* dy, const void*
   a.dbias = dbias;
   a.scratch = scratch_of(ws);
   a.status = static_cast<Status*>(ws);
-  return cuda_status(linear_grad_launch(a, sms, (cudaStream_t)stream));
+  return cuda_status(linear_grad_launch(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

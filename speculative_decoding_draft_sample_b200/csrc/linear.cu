@@ -16,17 +16,19 @@
 // Persistent pairs of CTAs (cta_group::2: one matrix instruction of 256 lanes
 // uses both SMs' tensor cores, each SM holding its 128 lanes of A and of the
 // result and half of B's columns, so every B byte enters one SM only) take work
-// units (output tile, part of the contraction):
+// units (an output tile or part of its contraction):
 //   warp 0     TMA producer: 128-byte-wide boxes of this CTA's A and B into a ring
 //              of stages; the bytes of both CTAs complete on the first one's barrier
 //   warp 1     tensor-memory allocation and, in the first CTA, the single-thread
 //              tcgen05.mma issuer
-//   warps 2-17 epilogue of the previous unit meanwhile (two accumulators): a warp
-//              reads its quarter of the lanes (hardware: warp index mod 4), the four
+//   warps 2-9  epilogue of the previous unit meanwhile (two accumulators): a warp
+//              reads its quarter of the lanes (hardware: warp index mod 4), the two
 //              warps of a quarter take blocks of 32 columns in turn
-// With fewer tiles than pairs the contraction is split: each part leaves its fp32
-// sums in the workspace and the last to arrive adds them in order of the parts
-// (the result does not depend on who that is) and finishes the tile.
+// Tiles that do not fill the pairs evenly are shared out by blocks of their
+// contraction: every pair takes an equal run of blocks, and where a tile's blocks
+// fall to several pairs, each leaves its fp32 sums in the workspace and the last
+// to arrive adds them in the order of the blocks (the result does not depend on
+// who that is) and finishes the tile. No pair waits for another.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
 #include "host.cuh"
 #include "linear.cuh"
@@ -39,7 +41,7 @@ namespace {
 
 using namespace t5;
 
-constexpr int kEpiWarps = 16;                  // four per quarter of the lanes, so that the latencies of a chunk overlap
+constexpr int kEpiWarps = 8;                   // two per quarter of the lanes (more would halve the registers of a thread)
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 64 + kEpiThreads;
 constexpr int kTileF = 256;                    // lanes: output features per tile, 128 in each CTA of the pair
@@ -69,7 +71,8 @@ struct Gemm {
   int F, T;                 // lanes (contiguous outputs) and columns in all
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
   int nt;                   // columns per tile, a multiple of 16 (128 when B is column-contiguous)
-  int tiles_f, tiles_t, splits;
+  int tiles_f, tiles_t;
+  int whole;                // tiles taken whole, the same number by every pair; the rest are shared by blocks
   const float* col_scale;   // [T] or null
   const float* lane_scale;  // [F] or null
   const float* bias;        // [F] or null
@@ -77,9 +80,8 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  int staged;               // bf16 rows of whole 16-byte vectors: through shared memory
-  float* partial;           // [tile, split, 2, nt rounded up to 32, 128] (splits > 1)
-  unsigned int* counter;    // [tile, CTA of the pair], zero at launch (splits > 1)
+  float* partial;           // [pair, 2, CTA, chunk, value, lane] sums of parts of shared tiles
+  unsigned int* counter;    // [shared tile, CTA], zero at launch
   Status* status;
 };
 
@@ -98,46 +100,47 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
   return g + z * g * (1.f - g) * dv;
 }
 
-__device__ __forceinline__ void activate32(float* v, int act) {
+template <int N>
+__device__ __forceinline__ void activate(float* v, int act) {
   if (act == DSPARK_ACT_RELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];  // NaN stays
+    for (int j = 0; j < N; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];  // NaN stays
   } else if (act == DSPARK_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = gate(v[j], v[j]);
+    for (int j = 0; j < N; ++j) v[j] = gate(v[j], v[j]);
   } else if (act == DSPARK_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = gate(v[j], kGelu2 * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
+    for (int j = 0; j < N; ++j) v[j] = gate(v[j], kGelu2 * fmaf(0.044715f * v[j] * v[j], v[j], v[j]));
   }
 }
 
-// fp32 outputs (and 2-byte rows that are not whole 16-byte vectors): one lane's
-// columns straight to memory, 32 neighbouring outputs per warp and store. All
+// fp32 outputs (and 2-byte rows that are not whole 16-byte vectors): 16 columns
+// of one lane straight to memory, 32 neighbouring outputs per warp and store. All
 // loads come before the first store: a load behind a store that might alias it
 // waits for its turn. at: column 0; n columns.
 template <int DT>
-__device__ __forceinline__ void direct32(const Gemm& g, float* v, long long at, int n) {
+__device__ __forceinline__ void direct16(const Gemm& g, float* v, long long at, int n) {
   using T = typename Elem<DT>::T;
   if (g.pre) {
     T* p = static_cast<T*>(g.pre) + at;
 #pragma unroll
-    for (int j = 0; j < 32; ++j, p += g.F)
+    for (int j = 0; j < 16; ++j, p += g.F)
       if (j < n) *p = Elem<DT>::store_round(v[j]);
   }
-  activate32(v, g.act);
+  activate<16>(v, g.act);
   if (g.residual) {
     const T* p = static_cast<const T*>(g.residual) + at;
-    T res[32];
+    T res[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j, p += g.F)
+    for (int j = 0; j < 16; ++j, p += g.F)
       if (j < n) res[j] = *p;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < 16; ++j)
       if (j < n) v[j] += Elem<DT>::to_float(res[j]);
   }
   T* p = static_cast<T*>(g.out) + at;
 #pragma unroll
-  for (int j = 0; j < 32; ++j, p += g.F)
+  for (int j = 0; j < 16; ++j, p += g.F)
     if (j < n) *p = Elem<DT>::store_round(v[j]);
 }
 
@@ -169,53 +172,83 @@ __device__ __forceinline__ void move_rows(unsigned char* stage, uint16_t* p, int
   }
 }
 
-// The work units of a pair, u = pair, pair + pairs, ...: unit u is part
-// u % splits of tile u / splits, and tiles run over the columns first, so that
-// pairs working at the same time share their rows of A. Steps by additions: a
-// unit of a short contraction lasts less than four divisions in a row.
+// The work units of a pair: first whole tiles pair, pair + pairs, ... < whole,
+// then an equal run of the blocks of the remaining ("shared") tiles, cut at tile
+// borders. Tiles run over the columns first, so that pairs working at the same
+// time share their rows of A. Whole tiles step by additions: a unit of a short
+// contraction lasts less than four divisions in a row.
 struct Units {
-  int u, left, sp, tt, tf;
-  int dsp, dtt, dtf, splits, tiles_t;
-  __device__ __forceinline__ Units(const Gemm& g, int pair, int pairs)
-      : u(pair), splits(g.splits), tiles_t(g.tiles_t) {
-    const int units = g.tiles_f * g.tiles_t * g.splits;
-    left = units > pair ? (units - pair + pairs - 1) / pairs : 0;
-    sp = pair % splits;
-    tt = pair / splits % tiles_t;
-    tf = pair / splits / tiles_t;
-    dsp = pairs % splits;
-    dtt = pairs / splits % tiles_t;
-    dtf = pairs / splits / tiles_t;
-  }
-  __device__ __forceinline__ void next() {
-    --left;
-    sp += dsp;
-    tt += dtt;
-    tf += dtf;
-    if (sp >= splits) {
-      sp -= splits;
-      ++tt;
-    }
-    if (tt >= tiles_t) {
-      tt -= tiles_t;
-      ++tf;
+  int tf, tt;          // the tile
+  int k0, k1;          // its blocks [k0, k1)
+  int shared;          // index among the shared tiles, or -1
+  int whole_left, dtt, dtf;
+  long long pos, end;  // blocks of the shared tiles left to this pair
+
+  __device__ __forceinline__ Units(const Gemm& g, int pair, int pairs) {
+    const long long blocks = (long long)(g.tiles_f * g.tiles_t - g.whole) * g.kblocks;
+    pos = blocks * pair / pairs;
+    end = blocks * (pair + 1) / pairs;
+    whole_left = g.whole > pair ? (g.whole - pair + pairs - 1) / pairs : 0;
+    dtt = pairs % g.tiles_t;
+    dtf = pairs / g.tiles_t;
+    if (whole_left > 0) {
+      set_tile(g, pair);
+      k0 = 0;
+      k1 = g.kblocks;
+      shared = -1;
+    } else {
+      start_shared(g);
     }
   }
-  // the part's blocks of the contraction
-  __device__ __forceinline__ void blocks(const Gemm& g, int& k0, int& k1) const {
-    k0 = 0;
-    k1 = g.kblocks;
-    if (splits > 1) {
-      k0 = (int)((long long)g.kblocks * sp / splits);
-      k1 = (int)((long long)g.kblocks * (sp + 1) / splits);
+  __device__ __forceinline__ bool more() const { return whole_left > 0 || pos < end; }
+  __device__ __forceinline__ void next(const Gemm& g) {
+    if (whole_left > 1) {
+      --whole_left;
+      tt += dtt;
+      tf += dtf;
+      if (tt >= g.tiles_t) {
+        tt -= g.tiles_t;
+        ++tf;
+      }
+    } else if (whole_left == 1) {
+      whole_left = 0;
+      start_shared(g);
+    } else {
+      pos += k1 - k0;
+      ++shared;
+      if (++tt >= g.tiles_t) {
+        tt -= g.tiles_t;
+        ++tf;
+      }
+      k0 = 0;
+      k1 = (int)min((long long)g.kblocks, end - pos);
     }
+  }
+
+ private:
+  __device__ __forceinline__ void set_tile(const Gemm& g, int tile) {
+    tt = tile % g.tiles_t;
+    tf = tile / g.tiles_t;
+  }
+  __device__ __forceinline__ void start_shared(const Gemm& g) {
+    shared = (int)(pos / g.kblocks);
+    set_tile(g, g.whole + shared);
+    k0 = (int)(pos - (long long)shared * g.kblocks);
+    k1 = (int)min((long long)g.kblocks, k0 + end - pos);
   }
 };
 
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// Which pairs hold blocks of shared tile s: the one of its first block to the one
+// of its last (run p is [blocks p / pairs, blocks (p + 1) / pairs)).
+__device__ __forceinline__ int pair_of_block(long long block, long long blocks, int pairs) {
+  return (int)(((block + 1) * pairs - 1) / blocks);
+}
+
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 // A_MN / B_MN: the operand is contiguous along lanes / columns, not along the contraction.
-template <bool F8, bool A_MN, bool B_MN>
+// STAGED: bf16 rows of whole 16-byte vectors, through shared memory.
+template <bool F8, bool A_MN, bool B_MN, bool STAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm g) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -270,12 +303,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
       int s = 0, issued = 0;
       uint32_t ph = 1;
-      for (; w.left > 0 && !*dead; w.next()) {
+      for (; w.more() && !*dead; w.next(g)) {
         const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt + rank * nh;
-        int k0, k1;
-        w.blocks(g, k0, k1);
-        int kx = k0 * (F8 ? 128 : 64);
-        for (int kb = k0; kb < k1; ++kb, kx += F8 ? 128 : 64) {
+        int kx = w.k0 * (F8 ? 128 : 64);
+        for (int kb = w.k0; kb < w.k1; ++kb, kx += F8 ? 128 : 64) {
           if (!mbar_wait(&empty[s], ph)) {
             if (!*dead) report_wait(g.status, kWhereEmpty, 0);
             *dead = 1;
@@ -318,9 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, done = 0;
       uint32_t ph = 0, aph = 1, buf = 0;
       uint64_t da = desc_a, db = desc_b;
-      for (; w.left > 0 && !*dead; w.next()) {
-        int k0, k1;
-        w.blocks(g, k0, k1);
+      for (; w.more() && !*dead; w.next(g)) {
         if (!mbar_wait(&acc_empty[buf], aph)) {
           if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
           *dead = 1;
@@ -329,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_after();
         const uint32_t d = tmem + buf * kMaxCols;
         uint32_t acc = 0;
-        for (int kb = k0; kb < k1; ++kb) {
+        for (int kb = w.k0; kb < w.k1; ++kb) {
           if (!mbar_wait(&full[s], ph)) {
             if (!*dead) report_wait(g.status, kWhereFull, 0);
             *dead = 1;
@@ -368,92 +397,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     unsigned char* stage = smem + kOffStage + (warp - 2) * kStageBytes;
     const uint32_t mat = su32(stage) + stage_at(lane & 7, lane >> 3);  // + 512 for the next 8 columns
     // the features whose values this thread holds: one lane's, or four rows of its fragments
-    const int nrow = g.staged ? 4 : 1, row0 = g.staged ? quarter * 32 + (lane >> 2) : ln;
-    float ls[4], bias[4];
+    constexpr int kRows = STAGED ? 4 : 1;
+    constexpr int kCols = STAGED ? kChunk : 16;     // columns that a warp takes at a time
+    constexpr int kStep = kEpiWarps / 4 * kCols;
+    const int row0 = STAGED ? quarter * 32 + (lane >> 2) : ln;
+    // the first column (of any thread) that values j .. j + 3 belong to
+    auto column_of = [](int j) { return STAGED ? 2 * (j & 12) : j; };
+    float ls[kRows], bias[kRows];
 
-    // 32 columns from c of the tile to the outputs; cscale: lane j's is column j's scale
+    // columns c .. c + kCols - 1 of the tile to the outputs; cscale: lane j's is column j's scale
     auto finish = [&](float* v, int f0, int t0, int c, float cscale) {
-      if (!g.staged) {
+      const int cols = min(min(kCols, g.nt - c), g.T - t0 - c);
+      if constexpr (!STAGED) {
         if (g.lane_scale) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= ls[0] * __shfl_sync(0xffffffffu, cscale, j);
+          for (int j = 0; j < kCols; ++j) v[j] *= ls[0] * __shfl_sync(0xffffffffu, cscale, j);
         }
         if (g.bias) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] += bias[0];
+          for (int j = 0; j < kCols; ++j) v[j] += bias[0];
         }
-        const int n = f0 + ln < g.F ? min(min(kChunk, g.nt - c), g.T - t0 - c) : 0;
+        const int n = f0 + ln < g.F ? cols : 0;
         const long long at = (long long)(t0 + c) * g.F + f0 + ln;
         if (g.out_type == DSPARK_F32)
-          direct32<DSPARK_F32>(g, v, at, n);
+          direct16<DSPARK_F32>(g, v, at, n);
         else
-          direct32<DSPARK_BF16>(g, v, at, n);
-        return;
-      }
-      if (g.lane_scale) {
+          direct16<DSPARK_BF16>(g, v, at, n);
+      } else {
+        if (g.lane_scale) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = __shfl_sync(0xffffffffu, cscale, 8 * k + 2 * (lane & 3) + e);
+            for (int e = 0; e < 2; ++e) {
+              const float s = __shfl_sync(0xffffffffu, cscale, 8 * k + 2 * (lane & 3) + e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[16 * (i >> 1) + 4 * k + 2 * (i & 1) + e] *= ls[i] * s;
+              for (int i = 0; i < 4; ++i) v[16 * (i >> 1) + 4 * k + 2 * (i & 1) + e] *= ls[i] * s;
+            }
           }
         }
-      }
-      if (g.bias) {
+        if (g.bias) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += bias[2 * (j >> 4) + ((j >> 1) & 1)];
-      }
-      const int rows = min(min(kChunk, g.nt - c), g.T - t0 - c), fw = f0 + quarter * 32;
-      const long long at = (long long)(t0 + c) * g.F + fw;
-      auto put = [&](void* p) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
-            w[i] = pack_bf16x2(a[0], a[1]);
-          }
-          store_matrix_t(mat + k * 512, w);
+          for (int j = 0; j < kCols; ++j) v[j] += bias[2 * (j >> 4) + ((j >> 1) & 1)];
         }
-        __syncwarp();
-        move_rows<true>(stage, static_cast<uint16_t*>(p) + at, g.F, g.F - fw, rows, lane);
-        __syncwarp();  // the stage is free again
-      };
-      if (g.pre) put(g.pre);
-      activate32(v, g.act);
-      if (g.residual) {
-        move_rows<false>(stage, const_cast<uint16_t*>(static_cast<const uint16_t*>(g.residual)) + at, g.F, g.F - fw, rows, lane);
-        __syncwarp();
+        const int fw = f0 + quarter * 32;
+        const long long at = (long long)(t0 + c) * g.F + fw;
+        auto put = [&](void* p) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
-          load_matrix_t(mat + k * 512, w);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t q[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
-            a[0] += __uint_as_float(w[i] << 16);
-            a[1] += __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {
+              const float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+              q[i] = pack_bf16x2(a[0], a[1]);
+            }
+            store_matrix_t(mat + k * 512, q);
           }
+          __syncwarp();
+          move_rows<true>(stage, static_cast<uint16_t*>(p) + at, g.F, g.F - fw, cols, lane);
+          __syncwarp();  // the stage is free again
+        };
+        if (g.pre) put(g.pre);
+        activate<kCols>(v, g.act);
+        if (g.residual) {
+          move_rows<false>(stage, const_cast<uint16_t*>(static_cast<const uint16_t*>(g.residual)) + at, g.F, g.F - fw, cols,
+                           lane);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t q[4];
+            load_matrix_t(mat + k * 512, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float* a = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+              a[0] += __uint_as_float(q[i] << 16);
+              a[1] += __uint_as_float(q[i] & 0xffff0000u);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        put(g.out);
       }
-      put(g.out);
     };
 
     // A warp whose wait gives up goes on without its work: the barriers of a
-    // split contraction expect every warp.
+    // shared tile expect every warp.
     uint32_t buf = 0, aph = 0;
-    for (; w.left > 0; w.next()) {
+    for (; w.more(); w.next(g)) {
       const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int f = f0 + row0 + 8 * i;
-        const bool in = i < nrow && f < g.F;
-        ls[i] = g.lane_scale && in ? __ldg(g.lane_scale + f) : 0.f;
-        bias[i] = g.bias && in ? __ldg(g.bias + f) : 0.f;
+        ls[i] = g.lane_scale && f < g.F ? __ldg(g.lane_scale + f) : 0.f;
+        bias[i] = g.bias && f < g.F ? __ldg(g.bias + f) : 0.f;
       }
       bool ok = !*dead;
       if (ok && !mbar_wait(&acc_full[buf], aph)) {
@@ -464,47 +499,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
-      // partial sums in the threads' own order: [tile, split, CTA, chunk, value, lane]
-      const int chunks = (g.nt + kChunk - 1) / kChunk, tile = w.tf * g.tiles_t + w.tt;
-      float* part = g.partial + ((size_t)tile * g.splits * 2 + rank) * chunks * (kChunk * 128) + ln;
-      const size_t part_split = (size_t)2 * chunks * (kChunk * 128);
       const int c1 = ok ? min(g.nt, g.T - t0) : 0;
-      for (int c = group * kChunk; c < c1; c += kEpiWarps / 4 * kChunk) {
-        float v[32];
+      const bool parted = w.k1 - w.k0 < g.kblocks;
+      // a pair holds at most one tile's first blocks without its last ones (slot 1)
+      // and one tile's later blocks (slot 0)
+      const size_t slot_floats = (size_t)(g.nt + kChunk - 1) / kChunk * (kChunk * 128);
+      float* mine = parted ? g.partial + ((size_t)(2 * pair + (w.k0 == 0)) * 2 + rank) * slot_floats + ln : nullptr;
+      for (int c = group * kCols; c < c1; c += kStep) {
+        float v[kCols];
         const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
-        if (g.staged)
+        if constexpr (STAGED)
           tmem_ld_frags(src + c, v);
         else
           tmem_ld_lanes(src + c, v);
-        if (c + kEpiWarps / 4 * kChunk >= c1) {  // the warp's last chunk: its part of the accumulator is free
+        if (c + kStep >= c1) {  // the warp's last chunk: its part of the accumulator is free
           fence_before();
           if (lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);
         }
-        if (g.splits == 1) {
+        if (!parted) {
           finish(v, f0, t0, c, cscale);
         } else {
-          float* p = part + w.sp * part_split + (size_t)(c / kChunk) * (kChunk * 128);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) p[j * 128] = v[j];
+          for (int j = 0; j < kCols; j += 4)
+            if (c + column_of(j) < c1) {
+#pragma unroll
+              for (int q = j; q < j + 4; ++q) mine[(size_t)(c + q) * 128] = v[q];
+            }
         }
       }
-      if (group * kChunk >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
-      if (g.splits > 1) {
+      if (group * kCols >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
+      if (parted) {
+        const long long first = (long long)w.shared * g.kblocks;
+        const long long blocks = (long long)(g.tiles_f * g.tiles_t - g.whole) * g.kblocks;
+        const int p0 = pair_of_block(first, blocks, pairs), p1 = pair_of_block(first + g.kblocks - 1, blocks, pairs);
         __threadfence();
         epi_bar();
-        if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * tile + rank], 1u) == (unsigned)g.splits - 1;
+        if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * w.shared + rank], 1u) == (unsigned)(p1 - p0);
         epi_bar();
         if (*(volatile int*)last_flag) {
           __threadfence();
-          for (int c = group * kChunk; c < c1; c += kEpiWarps / 4 * kChunk) {
+          for (int c = group * kCols; c < c1; c += kStep) {
             const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
-            const float* p = part + (size_t)(c / kChunk) * (kChunk * 128);
-            float v[32];
+            float v[kCols];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            for (int q = 0; q < g.splits; ++q, p += part_split)
+            for (int j = 0; j < kCols; ++j) v[j] = 0.f;
+            const float* q = g.partial + ((size_t)(2 * p0 + 1) * 2 + rank) * slot_floats + ln + (size_t)c * 128;
+            for (int p = p0; p <= p1; ++p) {
+              float d[kCols];  // loaded together: one wait per part
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += __ldcg(p + j * 128);
+              for (int j = 0; j < kCols; j += 4)
+                if (c + column_of(j) < c1) {
+#pragma unroll
+                  for (int e = j; e < j + 4; ++e) d[e] = __ldcg(q + e * 128);
+                }
+#pragma unroll
+              for (int j = 0; j < kCols; j += 4)
+                if (c + column_of(j) < c1) {
+#pragma unroll
+                  for (int e = j; e < j + 4; ++e) v[e] += d[e];
+                }
+              q = g.partial + ((size_t)(2 * (p + 1)) * 2 + rank) * slot_floats + ln + (size_t)c * 128;
+            }
             finish(v, f0, t0, c, cscale);
           }
         }
@@ -569,37 +624,56 @@ __global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* p
 // host: how the work is cut
 // ---------------------------------------------------------------------------
 struct Plan {
-  int nt, tiles_f, tiles_t, splits;
-  size_t partial_bytes() const {
-    return splits > 1 ? (size_t)tiles_f * tiles_t * splits * round_up(nt, kChunk) * kTileF * sizeof(float) : 0;
-  }
-  size_t counter_bytes() const { return splits > 1 ? round_up((size_t)tiles_f * tiles_t * 2 * sizeof(unsigned int), 256) : 0; }
-  size_t bytes() const { return counter_bytes() + round_up(partial_bytes(), 256); }
+  int nt, tiles_f, tiles_t;
+  int whole;   // tiles that the pairs take whole
+  int pairs;   // pairs of CTAs launched
+  int shared() const { return tiles_f * tiles_t - whole; }
+  size_t counter_bytes() const { return shared() ? round_up((size_t)shared() * 2 * sizeof(unsigned int), 256) : 0; }
+  size_t partial_bytes() const { return shared() ? (size_t)pairs * 2 * round_up(nt, kChunk) * kTileF * sizeof(float) : 0; }
+  size_t bytes() const { return counter_bytes() + partial_bytes(); }
 };
 
-// The column width and the split of the contraction with the least time by a
-// count of cycles: a 128-byte block of a stage costs its bytes at 64 a cycle or
-// its matrix instructions (nt / 2 cycles each), whichever is more; a unit adds
-// a fixed start and end.
-Plan make_plan(long long F, long long T, int kblocks, int min_nt) {
+// The column width and the sharing of the tiles with the least time by a count
+// of cycles: a block of a stage costs its bytes at kFeed a cycle and SM or its
+// matrix instructions (nt / 2 cycles each), whichever is more; the last tile's
+// epilogue is not hidden, and joining shared tiles costs about a write and a read
+// of the sums.
+Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
+  constexpr int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};
+  constexpr double kFeed = 64.0;
   Plan best = {};
   double best_cost = 1e300;
-  for (int nt = min_nt; nt <= kMaxCols; nt *= 2) {
+  for (int nt : kWidths) {
+    if (b_cols && nt % 128 != 0) continue;
     Plan p;
     p.nt = nt;
     p.tiles_f = (int)((F + kTileF - 1) / kTileF);
     p.tiles_t = (int)((T + nt - 1) / nt);
-    const long long tiles = (long long)p.tiles_f * p.tiles_t;
-    p.splits = (int)(tiles < kPlanPairs ? kPlanPairs / tiles : 1);
-    if (p.splits > kblocks / 4) p.splits = kblocks / 4;
-    if (p.splits < 1) p.splits = 1;
-    const long long waves = (tiles * p.splits + kPlanPairs - 1) / kPlanPairs;
-    const double block = fmax((kABytes + nt * 64) / 64.0, 2.0 * nt);
-    const double unit = (double)((kblocks + p.splits - 1) / p.splits) * block + 1500 + 8.0 * nt * (p.splits > 1 ? 2 : 1);
-    const double cost = waves * unit;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = p;
+    const int tiles = p.tiles_f * p.tiles_t;
+    const double block = fmax((kABytes + nt * 64) / kFeed, 2.0 * nt), edge = 4000 + 20.0 * nt, join = 4000 + 20.0 * nt;
+    for (int share = 0; share < 3; ++share) {
+      double cost;
+      if (share == 0) {  // every tile whole
+        p.pairs = min(tiles, kPlanPairs);
+        p.whole = tiles;
+        cost = (double)((tiles + p.pairs - 1) / p.pairs) * kblocks * block + edge;
+      } else if (share == 1) {  // full rounds whole but the last, which is shared with the remainder
+        if (tiles % kPlanPairs == 0) continue;
+        p.whole = max(0, tiles / kPlanPairs - 1) * kPlanPairs;
+        const long long blocks = (long long)p.shared() * kblocks;
+        p.pairs = p.whole ? kPlanPairs : (int)max(1LL, min((long long)kPlanPairs, blocks / 4));
+        cost = ((double)p.whole / p.pairs * kblocks + (double)((blocks + p.pairs - 1) / p.pairs)) * block + edge + 2 * join;
+      } else {  // every tile shared by the same number of pairs
+        const int parts = min(kPlanPairs / tiles, kblocks / 4);
+        if (parts < 2) continue;
+        p.whole = 0;
+        p.pairs = tiles * parts;
+        cost = (double)((kblocks + parts - 1) / parts) * block + edge + join;
+      }
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = p;
+      }
     }
   }
   return best;
@@ -608,10 +682,10 @@ Plan make_plan(long long F, long long T, int kblocks, int min_nt) {
 inline int kblocks_of(long long bytes_or_rows, int per) { return (int)((bytes_or_rows + per - 1) / per); }
 
 Plan plan_forward(int M, int N, int K, int in_type) {
-  return make_plan(N, M, in_type == DSPARK_E4M3 ? kblocks_of(K, 128) : kblocks_of(K, 64), 16);
+  return make_plan(N, M, kblocks_of((long long)K * (in_type == DSPARK_E4M3 ? 1 : 2), 128), false);
 }
-Plan plan_dx(int M, int N, int K) { return make_plan(K, M, kblocks_of(N, 64), 16); }
-Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), 128); }
+Plan plan_dx(int M, int N, int K) { return make_plan(K, M, kblocks_of(N, 64), false); }
+Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), true); }
 
 // Row runs of dpre_kernel: enough CTAs for two on every SM, 64 rows or more each.
 inline int dpre_runs(int M, int N) {
@@ -619,26 +693,23 @@ inline int dpre_runs(int M, int N) {
   return max(1, min((M + 63) / 64, (4 * kPlanPairs + cols - 1) / cols));
 }
 
-template <bool F8, bool A_MN, bool B_MN>
-cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, char* scratch, int num_sms,
-                        cudaStream_t s) {
+template <bool F8, bool A_MN, bool B_MN, bool STAGED>
+cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, char* scratch, cudaStream_t s) {
   g.nt = p.nt;
   g.tiles_f = p.tiles_f;
   g.tiles_t = p.tiles_t;
-  g.splits = p.splits;
-  g.staged = g.out_type == DSPARK_BF16 && g.F % 8 == 0 && aligned16(g.out) && aligned16(g.residual) && aligned16(g.pre);
+  g.whole = p.whole;
   cudaError_t e;
-  if (p.splits > 1) {
+  if (p.shared()) {
     g.counter = reinterpret_cast<unsigned int*>(scratch);
     g.partial = reinterpret_cast<float*>(scratch + p.counter_bytes());
     e = cudaMemsetAsync(g.counter, 0, p.counter_bytes(), s);
     if (e != cudaSuccess) return e;
   }
-  auto kern = linear_kernel<F8, A_MN, B_MN>;
+  auto kern = linear_kernel<F8, A_MN, B_MN, STAGED>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const long long units = (long long)p.tiles_f * p.tiles_t * p.splits;
-  kern<<<2 * (unsigned)min(units, (long long)num_sms / 2), kThreads, kSmem, s>>>(ma, mb, g);
+  kern<<<2 * p.pairs, kThreads, kSmem, s>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
@@ -654,7 +725,7 @@ size_t linear_scratch_bytes(int M, int N, int K, int in_type) {
   return n;
 }
 
-cudaError_t linear_launch(const LinearArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s) {
   const bool f8 = a.in_type == DSPARK_E4M3;
   const int es = f8 ? 1 : 2;
   const Plan p = plan_forward(a.M, a.N, a.K, a.in_type);
@@ -673,11 +744,15 @@ cudaError_t linear_launch(const LinearArgs& a, int num_sms, cudaStream_t s) {
   g.out_type = a.out_type;
   g.act = a.act;
   g.status = a.status;
-  return f8 ? gemm_launch<true, false, false>(g, p, ma, mb, a.scratch, num_sms, s)
-            : gemm_launch<false, false, false>(g, p, ma, mb, a.scratch, num_sms, s);
+  const bool staged = g.out_type == DSPARK_BF16 && g.F % 8 == 0 && aligned16(g.out) && aligned16(g.residual) && aligned16(g.pre);
+  if (f8)
+    return staged ? gemm_launch<true, false, false, true>(g, p, ma, mb, a.scratch, s)
+                  : gemm_launch<true, false, false, false>(g, p, ma, mb, a.scratch, s);
+  return staged ? gemm_launch<false, false, false, true>(g, p, ma, mb, a.scratch, s)
+                : gemm_launch<false, false, false, false>(g, p, ma, mb, a.scratch, s);
 }
 
-cudaError_t linear_grad_launch(const LinearGradArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   const Plan px = plan_dx(a.M, a.N, a.K), pw = plan_dw(a.M, a.N, a.K);
   char* split = a.scratch;
   char* dpre_buf = split + max(px.bytes(), pw.bytes());
@@ -704,14 +779,14 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, int num_sms, cudaStream_
     g.T = a.M;
     g.kblocks = kblocks_of(a.N, 64);
     g.out = a.dx;
-    if ((e = gemm_launch<false, true, false>(g, px, ma, mb, split, num_sms, s)) != cudaSuccess) return e;
+    if ((e = gemm_launch<false, true, false, true>(g, px, ma, mb, split, s)) != cudaSuccess) return e;
   }
   if (a.dw) {  // lanes k, columns n, contraction m
     if (!make_map(&ma, a.x, 2, a.K, a.M, 64) || !make_map(&mb, dpre, 2, a.N, a.M, 64)) return cudaErrorInvalidValue;
     g.T = a.N;
     g.kblocks = kblocks_of(a.M, 64);
     g.out = a.dw;
-    if ((e = gemm_launch<false, true, true>(g, pw, ma, mb, split, num_sms, s)) != cudaSuccess) return e;
+    if ((e = gemm_launch<false, true, true, true>(g, pw, ma, mb, split, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -36,7 +36,7 @@ struct LinearGradArgs {
 
 // Workspace past the status block, for the forward and the backward call.
 size_t linear_scratch_bytes(int M, int N, int K, int in_type);
-cudaError_t linear_launch(const LinearArgs& a, int num_sms, cudaStream_t s);
-cudaError_t linear_grad_launch(const LinearGradArgs& a, int num_sms, cudaStream_t s);
+cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s);
+cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s);
 
 }  // namespace dspark

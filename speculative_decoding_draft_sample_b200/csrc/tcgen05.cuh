@@ -100,20 +100,19 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 
 #define DSPARK_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
 
-// 32 accumulator columns of this warp's 32 lanes: v[j] is column j of lane `lane`.
+// 16 accumulator columns of this warp's 32 lanes: v[j] is column j of lane `lane`.
 __device__ __forceinline__ void tmem_ld_lanes(uint32_t taddr, float* v) {
-  uint32_t r[32];
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : DSPARK_R8(r, 0), DSPARK_R8(r, 8), DSPARK_R8(r, 16), DSPARK_R8(r, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : DSPARK_R8(r, 0), DSPARK_R8(r, 8)
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The same 32 x 32 block as 8 x 8 matrix fragments: v[16 h + 4 k + 2 i + e] is
+// 32 columns of 32 lanes as 8 x 8 matrix fragments: v[16 h + 4 k + 2 i + e] is
 // lane 16 h + 8 i + lane / 4, column 8 k + 2 (lane % 4) + e.
 __device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, float* v) {
   uint32_t r[32];
