@@ -294,24 +294,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // The producer and the issuer are one thread each, whose loop has to keep up
-  // with a block of 512 tensor-core cycles: stages and phases are counted, not
-  // divided, and addresses and descriptors advance by additions (a loop that
-  // computed them anew took 730 cycles a block).
+  // The producer's and the issuer's loop have to keep up with a block of 512
+  // tensor-core cycles: they run in a whole converged warp, of which one lane
+  // issues, stages and phases are counted, not divided, and addresses and
+  // descriptors advance by additions (a loop of one thread that computed them
+  // anew took 730 cycles a block).
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
-      int s = 0, issued = 0;
-      uint32_t ph = 1;
-      for (; w.more() && !*dead; w.next(g)) {
-        const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt + rank * nh;
-        int kx = w.k0 * (F8 ? 128 : 64);
-        for (int kb = w.k0; kb < w.k1; ++kb, kx += F8 ? 128 : 64) {
-          if (!mbar_wait(&empty[s], ph)) {
-            if (!*dead) report_wait(g.status, kWhereEmpty, 0);
-            *dead = 1;
-            break;
-          }
+    const bool lead = elect_one();
+    const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (; w.more() && ok; w.next(g)) {
+      const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt + rank * nh;
+      int kx = w.k0 * (F8 ? 128 : 64);
+      for (int kb = w.k0; kb < w.k1; ++kb, kx += F8 ? 128 : 64) {
+        ok = mbar_wait_warp(&empty[s], ph);
+        if (!ok) break;
+        if (lead) {
           if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
           const uint32_t bar = full0 + 8 * s;
           const uint32_t a = smem0 + s * stage_bytes, b = a + kABytes;
@@ -326,19 +326,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d(b, &map_b, kx, t0, bar);
           }
-          ++issued;
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      if (*dead && rank == 0)  // let issued loads of both CTAs land before the pair winds down (below)
+    }
+    if (!ok && lead) {
+      if (!*dead) report_wait(g.status, kWhereEmpty, 0);
+      *dead = 1;
+      if (rank == 0)  // let issued loads of both CTAs land before the pair winds down (below)
         for (int q = max(0, issued - stages); q < issued; ++q) mbar_wait(&full[q % stages], (q / stages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool lead = elect_one();
       // D fp32; A and B bf16 or e4m3; widths nt and 256
       const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) |
                              ((uint32_t)B_MN << 16) | ((uint32_t)(g.nt >> 3) << 17) | ((uint32_t)(kTileF >> 4) << 24);
@@ -349,28 +355,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, done = 0;
       uint32_t ph = 0, aph = 1, buf = 0;
       uint64_t da = desc_a, db = desc_b;
-      for (; w.more() && !*dead; w.next(g)) {
-        if (!mbar_wait(&acc_empty[buf], aph)) {
-          if (!*dead) report_wait(g.status, kWhereAccEmpty, 0);
-          *dead = 1;
-          break;
-        }
+      bool ok = true;
+      unsigned int site = kWhereAccEmpty;
+      for (; w.more(); w.next(g)) {
+        ok = mbar_wait_warp(&acc_empty[buf], aph);
+        if (!ok) break;
         fence_after();
         const uint32_t d = tmem + buf * kMaxCols;
         uint32_t acc = 0;
         for (int kb = w.k0; kb < w.k1; ++kb) {
-          if (!mbar_wait(&full[s], ph)) {
-            if (!*dead) report_wait(g.status, kWhereFull, 0);
-            *dead = 1;
-            break;
-          }
+          ok = mbar_wait_warp(&full[s], ph);
+          if (!ok) break;
           fence_after();
+          if (lead) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // 32 bytes of the contraction (or 16 rows of it) each
-            mma<F8>(d, da + q * step_a, db + q * step_b, idesc, acc);
-            acc = 1;
+            for (int q = 0; q < 4; ++q)  // 32 bytes of the contraction (or 16 rows of it) each
+              mma<F8>(d, da + q * step_a, db + q * step_b, idesc, q ? 1u : acc);
+            mma_commit(&empty[s]);
           }
-          mma_commit(&empty[s]);
+          __syncwarp();
+          acc = 1;
           ++done;
           da += stage_bytes >> 4;
           db += stage_bytes >> 4;
@@ -381,13 +385,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             db = desc_b;
           }
         }
-        if (*dead) break;
-        mma_commit(&acc_full[buf]);
+        if (!ok) {
+          site = kWhereFull;
+          break;
+        }
+        if (lead) mma_commit(&acc_full[buf]);
+        __syncwarp();
         buf ^= 1;
         if (buf == 0) aph ^= 1;
       }
-      if (*dead && done > 0)  // MMAs complete in order: after the last commit tensor memory is quiet
-        mbar_wait(&empty[(done - 1) % stages], ((done - 1) / stages) & 1);
+      if (!ok && lead) {
+        if (!*dead) report_wait(g.status, site, 0);
+        *dead = 1;
+        if (done > 0)  // MMAs complete in order: after the last commit tensor memory is quiet
+          mbar_wait(&empty[(done - 1) % stages], ((done - 1) / stages) & 1);
+      }
     }
     __syncwarp();
   } else {

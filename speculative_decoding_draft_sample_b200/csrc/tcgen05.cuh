@@ -44,6 +44,35 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t par) {
   }
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
+// The same wait by a whole warp, decided by a vote: what follows stays uniform,
+// so that descriptors and addresses live in the uniform registers that the
+// tensor-core and TMA instructions take them from.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t par) {
+  const uint32_t bar = su32(b);
+  unsigned long long start = 0;
+  for (unsigned it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(par)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((it & 255u) == 0) {
+      const unsigned long long now = global_ns();
+      if (start == 0) start = now;
+      if (__any_sync(0xffffffffu, now - start > kWaitLimitNs)) return false;
+    }
+  }
+}
+
 // Pair of CTAs (cta_group::2): one issues the matrix instructions for both.
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
