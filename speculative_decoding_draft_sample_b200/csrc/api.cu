@@ -90,7 +90,7 @@ size_t dspark_workspace_bytes(int op, int B, int K, int V, int r, int dtype) {
       return kStatusBytes + (size_t)kNormGradBlocks * V * sizeof(float);
     case DSPARK_OP_LINEAR:
       if (!linear_shape_ok(B, V, r, dtype)) return 0;
-      return kStatusBytes + linear_scratch_bytes(B, V, r, dtype);
+      return kStatusBytes + linear_scratch_bytes(B, V, dtype);
     default:
       return 0;
   }

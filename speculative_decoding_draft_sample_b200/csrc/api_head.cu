@@ -159,7 +159,6 @@ int dspark_linear(const void* x, const void* w, const float* x_scale, const floa
   a.act = act;
   a.y = y;
   a.pre = pre;
-  a.scratch = scratch_of(ws);
   a.status = static_cast<Status*>(ws);
   return cuda_status(linear_launch(a, (cudaStream_t)stream));
 }

@@ -24,11 +24,10 @@
 //   warps 2-9  epilogue of the previous unit meanwhile (two accumulators): a warp
 //              reads its quarter of the lanes (hardware: warp index mod 4), the two
 //              warps of a quarter take blocks of 32 columns in turn
-// Tiles that do not fill the pairs evenly are shared out by blocks of their
-// contraction: every pair takes an equal run of blocks, and where a tile's blocks
-// fall to several pairs, each leaves its fp32 sums in the workspace and the last
-// to arrive adds them in the order of the blocks (the result does not depend on
-// who that is) and finishes the tile. No pair waits for another.
+// With few tiles a cluster of 2, 4 or 8 pairs takes one tile, each pair a part of
+// the contraction; the other pairs leave their fp32 sums in the first one's shared
+// memory (its ring is free by then), which adds them in the order of the parts and
+// finishes the tile.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
 #include "host.cuh"
 #include "linear.cuh"
@@ -72,7 +71,7 @@ struct Gemm {
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
   int nt;                   // columns per tile, a multiple of 16 (128 when B is column-contiguous)
   int tiles_f, tiles_t;
-  int whole;                // tiles taken whole, the same number by every pair; the rest are shared by blocks
+  int parts;                // pairs that share a tile (1, 2, 4 or 8)
   const float* col_scale;   // [T] or null
   const float* lane_scale;  // [F] or null
   const float* bias;        // [F] or null
@@ -80,8 +79,6 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  float* partial;           // [pair, 2, CTA, chunk, value, lane] sums of parts of shared tiles
-  unsigned int* counter;    // [shared tile, CTA], zero at launch
   Status* status;
 };
 
@@ -172,84 +169,35 @@ __device__ __forceinline__ void move_rows(unsigned char* stage, uint16_t* p, int
   }
 }
 
-// The work units of a pair: first whole tiles pair, pair + pairs, ... < whole,
-// then an equal run of the blocks of the remaining ("shared") tiles, cut at tile
-// borders. Tiles run over the columns first, so that pairs working at the same
-// time share their rows of A. Whole tiles step by additions: a unit of a short
-// contraction lasts less than four divisions in a row.
-struct Units {
-  int tf, tt;          // the tile
-  int k0, k1;          // its blocks [k0, k1)
-  int shared;          // index among the shared tiles, or -1
-  int whole_left, dtt, dtf;
-  long long pos, end;  // blocks of the shared tiles left to this pair
-
-  __device__ __forceinline__ Units(const Gemm& g, int pair, int pairs) {
-    const long long blocks = (long long)(g.tiles_f * g.tiles_t - g.whole) * g.kblocks;
-    pos = blocks * pair / pairs;
-    end = blocks * (pair + 1) / pairs;
-    whole_left = g.whole > pair ? (g.whole - pair + pairs - 1) / pairs : 0;
-    dtt = pairs % g.tiles_t;
-    dtf = pairs / g.tiles_t;
-    if (whole_left > 0) {
-      set_tile(g, pair);
-      k0 = 0;
-      k1 = g.kblocks;
-      shared = -1;
-    } else {
-      start_shared(g);
-    }
+// The tiles of a pair: `first`, `first + step`, ... . Tiles run over the columns
+// first, so that pairs working at the same time share their rows of A. Steps by
+// additions: a tile of a short contraction lasts less than two divisions.
+struct Tiles {
+  int tf, tt, left, dtt, dtf;
+  __device__ __forceinline__ Tiles(const Gemm& g, int first, int step) {
+    const int tiles = g.tiles_f * g.tiles_t;
+    left = tiles > first ? (tiles - first + step - 1) / step : 0;
+    tt = first % g.tiles_t;
+    tf = first / g.tiles_t;
+    dtt = step % g.tiles_t;
+    dtf = step / g.tiles_t;
   }
-  __device__ __forceinline__ bool more() const { return whole_left > 0 || pos < end; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const Gemm& g) {
-    if (whole_left > 1) {
-      --whole_left;
-      tt += dtt;
-      tf += dtf;
-      if (tt >= g.tiles_t) {
-        tt -= g.tiles_t;
-        ++tf;
-      }
-    } else if (whole_left == 1) {
-      whole_left = 0;
-      start_shared(g);
-    } else {
-      pos += k1 - k0;
-      ++shared;
-      if (++tt >= g.tiles_t) {
-        tt -= g.tiles_t;
-        ++tf;
-      }
-      k0 = 0;
-      k1 = (int)min((long long)g.kblocks, end - pos);
+    --left;
+    tt += dtt;
+    tf += dtf;
+    if (tt >= g.tiles_t) {
+      tt -= g.tiles_t;
+      ++tf;
     }
-  }
-
- private:
-  __device__ __forceinline__ void set_tile(const Gemm& g, int tile) {
-    tt = tile % g.tiles_t;
-    tf = tile / g.tiles_t;
-  }
-  __device__ __forceinline__ void start_shared(const Gemm& g) {
-    shared = (int)(pos / g.kblocks);
-    set_tile(g, g.whole + shared);
-    k0 = (int)(pos - (long long)shared * g.kblocks);
-    k1 = (int)min((long long)g.kblocks, k0 + end - pos);
   }
 };
-
-// Which pairs hold blocks of shared tile s: the one of its first block to the one
-// of its last (run p is [blocks p / pairs, blocks (p + 1) / pairs)).
-__device__ __forceinline__ int pair_of_block(long long block, long long blocks, int pairs) {
-  return (int)(((block + 1) * pairs - 1) / blocks);
-}
-
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 // A_MN / B_MN: the operand is contiguous along lanes / columns, not along the contraction.
 // STAGED: bf16 rows of whole 16-byte vectors, through shared memory.
 template <bool F8, bool A_MN, bool B_MN, bool STAGED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm g) {
   extern __shared__ __align__(1024) unsigned char smem[];
   if (su32(smem) & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment (the same offset in every CTA)
@@ -262,16 +210,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  int* last_flag = abort_flag + 1;
   volatile int* dead = abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cta_rank();
+  const uint32_t cluster_rank = cta_rank(), rank = cluster_rank & 1;  // rank: CTA of the pair
+  const uint32_t first_rank = cluster_rank & ~1u;
+  const uint16_t both = (uint16_t)(3u << first_rank);
+  const int part = cluster_rank >> 1;  // the pair's part of the contraction
+  const int kb0 = (int)((long long)g.kblocks * part / g.parts), kb1 = (int)((long long)g.kblocks * (part + 1) / g.parts);
   const int nh = g.nt / 2;  // columns of B in this CTA
   const int stage_bytes = kABytes + nh * 128;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int stages = min(kMaxStages, kRing / stage_bytes);
-  Units w(g, pair, pairs);
+  Tiles w(g, blockIdx.x / (2 * g.parts), gridDim.x / (2 * g.parts));
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -301,14 +251,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // anew took 730 cycles a block).
   if (warp == 0) {
     const bool lead = elect_one();
-    const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), 0);
+    const uint32_t smem0 = su32(smem), full0 = map_rank(su32(full), first_rank);
     int s = 0, issued = 0;
     uint32_t ph = 1;
     bool ok = true;
     for (; w.more() && ok; w.next(g)) {
       const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt + rank * nh;
-      int kx = w.k0 * (F8 ? 128 : 64);
-      for (int kb = w.k0; kb < w.k1; ++kb, kx += F8 ? 128 : 64) {
+      int kx = kb0 * (F8 ? 128 : 64);
+      for (int kb = kb0; kb < kb1; ++kb, kx += F8 ? 128 : 64) {
         ok = mbar_wait_warp(&empty[s], ph);
         if (!ok) break;
         if (lead) {
@@ -363,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_after();
         const uint32_t d = tmem + buf * kMaxCols;
         uint32_t acc = 0;
-        for (int kb = w.k0; kb < w.k1; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = mbar_wait_warp(&full[s], ph);
           if (!ok) break;
           fence_after();
@@ -371,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)  // 32 bytes of the contraction (or 16 rows of it) each
               mma<F8>(d, da + q * step_a, db + q * step_b, idesc, q ? 1u : acc);
-            mma_commit(&empty[s]);
+            mma_commit(&empty[s], both);
           }
           __syncwarp();
           acc = 1;
@@ -389,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           site = kWhereFull;
           break;
         }
-        if (lead) mma_commit(&acc_full[buf]);
+        if (lead) mma_commit(&acc_full[buf], both);
         __syncwarp();
         buf ^= 1;
         if (buf == 0) aph ^= 1;
@@ -402,10 +352,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  }
+  const uint32_t slots = (uint32_t)((g.nt + kChunk - 1) / kChunk * kChunk) * kLanes * 4;  // bytes of one part's sums
+  if (g.parts > 1) {
+    // one tile per cluster: when every pair's products are complete the rings are
+    // free; sums of part q go to [q - 1, column, lane] of the first pair's
+    const int quarter = warp & 3;
+    const int c1 = min(g.nt, g.T - w.tt * g.nt);
+    if (warp >= 2 && !mbar_wait(&acc_full[0], 0)) {
+      if (!*dead) report_wait(g.status, kWhereAccFull, 0);
+      *dead = 1;
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && part > 0) {
+      fence_after();
+      const uint32_t to = map_rank(su32(smem), rank) + (part - 1) * slots + (quarter * 32 + lane) * 4;
+      for (int c = (warp - 2) / 4 * 16; c < c1; c += kEpiWarps / 4 * 16) {
+        float v[16];
+        tmem_ld_lanes(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st_cluster(to + (c + j) * kLanes * 4, v[j]);
+      }
+      fence_before();
+    }
+    cluster_sync();
+  }
+  if (warp >= 2 && part == 0) {
     const int quarter = warp & 3, group = (warp - 2) >> 2;
     const int ln = quarter * 32 + lane;    // lane of this CTA's part of the tile
-    const uint32_t acc_free = map_rank(su32(acc_empty), 0);
+    const uint32_t acc_free = map_rank(su32(acc_empty), first_rank);
     unsigned char* stage = smem + kOffStage + (warp - 2) * kStageBytes;
     const uint32_t mat = su32(stage) + stage_at(lane & 7, lane >> 3);  // + 512 for the next 8 columns
     // the features whose values this thread holds: one lane's, or four rows of its fragments
@@ -413,8 +389,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kCols = STAGED ? kChunk : 16;     // columns that a warp takes at a time
     constexpr int kStep = kEpiWarps / 4 * kCols;
     const int row0 = STAGED ? quarter * 32 + (lane >> 2) : ln;
-    // the first column (of any thread) that values j .. j + 3 belong to
-    auto column_of = [](int j) { return STAGED ? 2 * (j & 12) : j; };
     float ls[kRows], bias[kRows];
 
     // columns c .. c + kCols - 1 of the tile to the outputs; cscale: lane j's is column j's scale
@@ -491,8 +465,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     };
 
-    // A warp whose wait gives up goes on without its work: the barriers of a
-    // shared tile expect every warp.
     uint32_t buf = 0, aph = 0;
     for (; w.more(); w.next(g)) {
       const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt;
@@ -508,15 +480,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!*dead) report_wait(g.status, kWhereAccFull, 0);
         *dead = 1;
       }
-      ok = __all_sync(0xffffffffu, ok);
+      if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
-      const int c1 = ok ? min(g.nt, g.T - t0) : 0;
-      const bool parted = w.k1 - w.k0 < g.kblocks;
-      // a pair holds at most one tile's first blocks without its last ones (slot 1)
-      // and one tile's later blocks (slot 0)
-      const size_t slot_floats = (size_t)(g.nt + kChunk - 1) / kChunk * (kChunk * 128);
-      float* mine = parted ? g.partial + ((size_t)(2 * pair + (w.k0 == 0)) * 2 + rank) * slot_floats + ln : nullptr;
+      const int c1 = min(g.nt, g.T - t0);
       for (int c = group * kCols; c < c1; c += kStep) {
         float v[kCols];
         const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
@@ -528,54 +495,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_before();
           if (lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);
         }
-        if (!parted) {
-          finish(v, f0, t0, c, cscale);
-        } else {
+        for (int q = 1; q < g.parts; ++q) {
+          const float* s = reinterpret_cast<const float*>(smem + (q - 1) * slots) + c * kLanes;
 #pragma unroll
-          for (int j = 0; j < kCols; j += 4)
-            if (c + column_of(j) < c1) {
-#pragma unroll
-              for (int q = j; q < j + 4; ++q) mine[(size_t)(c + q) * 128] = v[q];
-            }
-        }
-      }
-      if (group * kCols >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
-      if (parted) {
-        const long long first = (long long)w.shared * g.kblocks;
-        const long long blocks = (long long)(g.tiles_f * g.tiles_t - g.whole) * g.kblocks;
-        const int p0 = pair_of_block(first, blocks, pairs), p1 = pair_of_block(first + g.kblocks - 1, blocks, pairs);
-        __threadfence();
-        epi_bar();
-        if (tid == 64) *last_flag = atomicAdd(&g.counter[2 * w.shared + rank], 1u) == (unsigned)(p1 - p0);
-        epi_bar();
-        if (*(volatile int*)last_flag) {
-          __threadfence();
-          for (int c = group * kCols; c < c1; c += kStep) {
-            const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
-            float v[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) v[j] = 0.f;
-            const float* q = g.partial + ((size_t)(2 * p0 + 1) * 2 + rank) * slot_floats + ln + (size_t)c * 128;
-            for (int p = p0; p <= p1; ++p) {
-              float d[kCols];  // loaded together: one wait per part
-#pragma unroll
-              for (int j = 0; j < kCols; j += 4)
-                if (c + column_of(j) < c1) {
-#pragma unroll
-                  for (int e = j; e < j + 4; ++e) d[e] = __ldcg(q + e * 128);
-                }
-#pragma unroll
-              for (int j = 0; j < kCols; j += 4)
-                if (c + column_of(j) < c1) {
-#pragma unroll
-                  for (int e = j; e < j + 4; ++e) v[e] += d[e];
-                }
-              q = g.partial + ((size_t)(2 * (p + 1)) * 2 + rank) * slot_floats + ln + (size_t)c * 128;
-            }
-            finish(v, f0, t0, c, cscale);
+          for (int j = 0; j < kCols; ++j) {
+            if constexpr (STAGED)  // value j's column and lane in the fragments
+              v[j] += s[(8 * (j >> 2 & 3) + 2 * (lane & 3) + (j & 1)) * kLanes + quarter * 32 + 16 * (j >> 4) + 8 * (j >> 1 & 1) + (lane >> 2)];
+            else
+              v[j] += s[j * kLanes + ln];
           }
         }
+        finish(v, f0, t0, c, cscale);
       }
+      if (group * kCols >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
       buf ^= 1;
       if (buf == 0) aph ^= 1;
     }
@@ -637,51 +569,36 @@ __global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* p
 // ---------------------------------------------------------------------------
 struct Plan {
   int nt, tiles_f, tiles_t;
-  int whole;   // tiles that the pairs take whole
-  int pairs;   // pairs of CTAs launched
-  int shared() const { return tiles_f * tiles_t - whole; }
-  size_t counter_bytes() const { return shared() ? round_up((size_t)shared() * 2 * sizeof(unsigned int), 256) : 0; }
-  size_t partial_bytes() const { return shared() ? (size_t)pairs * 2 * round_up(nt, kChunk) * kTileF * sizeof(float) : 0; }
-  size_t bytes() const { return counter_bytes() + partial_bytes(); }
+  int parts;     // pairs per tile
+  int clusters;  // of 2 * parts CTAs
 };
 
-// The column width and the sharing of the tiles with the least time by a count
-// of cycles: a block of a stage costs its bytes at kFeed a cycle and SM or its
-// matrix instructions (nt / 2 cycles each), whichever is more; the last tile's
-// epilogue is not hidden, and joining shared tiles costs about a write and a read
-// of the sums.
+// The column width and the number of parts with the least time by measured costs
+// (ns at K = 1024 and 2048, 74 pairs): a block of the contraction takes 150 up to
+// 80 columns (the issuing loop), then 1.5 a column; a tile at least its epilogue;
+// the first loads and the last epilogue are not hidden; a joined tile has two
+// cluster barriers and the parts' sums on top.
 Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
   constexpr int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};
-  constexpr double kFeed = 64.0;
   Plan best = {};
   double best_cost = 1e300;
   for (int nt : kWidths) {
     if (b_cols && nt % 128 != 0) continue;
-    Plan p;
-    p.nt = nt;
-    p.tiles_f = (int)((F + kTileF - 1) / kTileF);
-    p.tiles_t = (int)((T + nt - 1) / nt);
-    const int tiles = p.tiles_f * p.tiles_t;
-    const double block = fmax((kABytes + nt * 64) / kFeed, 2.0 * nt), edge = 4000 + 20.0 * nt, join = 4000 + 20.0 * nt;
-    for (int share = 0; share < 3; ++share) {
-      double cost;
-      if (share == 0) {  // every tile whole
-        p.pairs = min(tiles, kPlanPairs);
-        p.whole = tiles;
-        cost = (double)((tiles + p.pairs - 1) / p.pairs) * kblocks * block + edge;
-      } else if (share == 1) {  // full rounds whole but the last, which is shared with the remainder
-        if (tiles % kPlanPairs == 0) continue;
-        p.whole = max(0, tiles / kPlanPairs - 1) * kPlanPairs;
-        const long long blocks = (long long)p.shared() * kblocks;
-        p.pairs = p.whole ? kPlanPairs : (int)max(1LL, min((long long)kPlanPairs, blocks / 4));
-        cost = ((double)p.whole / p.pairs * kblocks + (double)((blocks + p.pairs - 1) / p.pairs)) * block + edge + 2 * join;
-      } else {  // every tile shared by the same number of pairs
-        const int parts = min(kPlanPairs / tiles, kblocks / 4);
-        if (parts < 2) continue;
-        p.whole = 0;
-        p.pairs = tiles * parts;
-        cost = (double)((kblocks + parts - 1) / parts) * block + edge + join;
-      }
+    const double block = fmax(150.0, 20.0 + 1.5 * nt), epilogue = 600.0 + 9.5 * nt;
+    for (int parts = 1; parts <= 8; parts *= 2) {
+      const int slots = (nt + kChunk - 1) / kChunk * kChunk * kLanes * 4;
+      if (parts > 1 && (parts > kblocks || (parts - 1) * slots > kRing)) break;
+      Plan p;
+      p.nt = nt;
+      p.tiles_f = (int)((F + kTileF - 1) / kTileF);
+      p.tiles_t = (int)((T + nt - 1) / nt);
+      p.parts = parts;
+      const int tiles = p.tiles_f * p.tiles_t, at_once = kPlanPairs / parts;
+      if (parts > 1 && tiles > at_once) break;
+      p.clusters = min(tiles, at_once);
+      const double tile = (double)((kblocks + parts - 1) / parts) * block + 400.0;
+      const double cost = ((tiles + at_once - 1) / at_once) * fmax(tile, epilogue) + epilogue +
+                          (parts > 1 ? 1500.0 + 4.0 * nt * parts : 0.0);
       if (cost < best_cost) {
         best_cost = cost;
         best = p;
@@ -706,35 +623,36 @@ inline int dpre_runs(int M, int N) {
 }
 
 template <bool F8, bool A_MN, bool B_MN, bool STAGED>
-cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, char* scratch, cudaStream_t s) {
+cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t s) {
   g.nt = p.nt;
   g.tiles_f = p.tiles_f;
   g.tiles_t = p.tiles_t;
-  g.whole = p.whole;
-  cudaError_t e;
-  if (p.shared()) {
-    g.counter = reinterpret_cast<unsigned int*>(scratch);
-    g.partial = reinterpret_cast<float*>(scratch + p.counter_bytes());
-    e = cudaMemsetAsync(g.counter, 0, p.counter_bytes(), s);
-    if (e != cudaSuccess) return e;
-  }
+  g.parts = p.parts;
   auto kern = linear_kernel<F8, A_MN, B_MN, STAGED>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess && p.parts > 4)  // clusters of 16 are past the portable size
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  kern<<<2 * p.pairs, kThreads, kSmem, s>>>(ma, mb, g);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.clusters * 2 * p.parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * p.parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
 }
 
 }  // namespace
 
-size_t linear_scratch_bytes(int M, int N, int K, int in_type) {
-  size_t n = plan_forward(M, N, K, in_type).bytes();
-  if (in_type == DSPARK_BF16) {
-    const size_t split = max(plan_dx(M, N, K).bytes(), plan_dw(M, N, K).bytes());
-    const size_t grad = split + round_up((size_t)M * N * 2, 256) + round_up((size_t)dpre_runs(M, N) * N * sizeof(float), 256);
-    if (grad > n) n = grad;
-  }
-  return n;
+size_t linear_scratch_bytes(int M, int N, int in_type) {
+  if (in_type != DSPARK_BF16) return 0;
+  return round_up((size_t)M * N * 2, 256) + round_up((size_t)dpre_runs(M, N) * N * sizeof(float), 256);
 }
 
 cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s) {
@@ -758,16 +676,15 @@ cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s) {
   g.status = a.status;
   const bool staged = g.out_type == DSPARK_BF16 && g.F % 8 == 0 && aligned16(g.out) && aligned16(g.residual) && aligned16(g.pre);
   if (f8)
-    return staged ? gemm_launch<true, false, false, true>(g, p, ma, mb, a.scratch, s)
-                  : gemm_launch<true, false, false, false>(g, p, ma, mb, a.scratch, s);
-  return staged ? gemm_launch<false, false, false, true>(g, p, ma, mb, a.scratch, s)
-                : gemm_launch<false, false, false, false>(g, p, ma, mb, a.scratch, s);
+    return staged ? gemm_launch<true, false, false, true>(g, p, ma, mb, s)
+                  : gemm_launch<true, false, false, false>(g, p, ma, mb, s);
+  return staged ? gemm_launch<false, false, false, true>(g, p, ma, mb, s)
+                : gemm_launch<false, false, false, false>(g, p, ma, mb, s);
 }
 
 cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   const Plan px = plan_dx(a.M, a.N, a.K), pw = plan_dw(a.M, a.N, a.K);
-  char* split = a.scratch;
-  char* dpre_buf = split + max(px.bytes(), pw.bytes());
+  char* dpre_buf = a.scratch;
   float* partial = reinterpret_cast<float*>(dpre_buf + round_up((size_t)a.M * a.N * 2, 256));
   const void* dpre = a.act == DSPARK_ACT_NONE ? a.dy : dpre_buf;
   cudaError_t e;
@@ -791,14 +708,14 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
     g.T = a.M;
     g.kblocks = kblocks_of(a.N, 64);
     g.out = a.dx;
-    if ((e = gemm_launch<false, true, false, true>(g, px, ma, mb, split, s)) != cudaSuccess) return e;
+    if ((e = gemm_launch<false, true, false, true>(g, px, ma, mb, s)) != cudaSuccess) return e;
   }
   if (a.dw) {  // lanes k, columns n, contraction m
     if (!make_map(&ma, a.x, 2, a.K, a.M, 64) || !make_map(&mb, dpre, 2, a.N, a.M, 64)) return cudaErrorInvalidValue;
     g.T = a.N;
     g.kblocks = kblocks_of(a.M, 64);
     g.out = a.dw;
-    if ((e = gemm_launch<false, true, true, true>(g, pw, ma, mb, split, s)) != cudaSuccess) return e;
+    if ((e = gemm_launch<false, true, true, true>(g, pw, ma, mb, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -17,7 +17,6 @@ struct LinearArgs {
   int in_type, out_type, act;
   void* y;                // [M, N] out_type
   void* pre;              // [M, N] out_type or null
-  char* scratch;          // linear_scratch_bytes() behind the status block
   Status* status;
 };
 
@@ -30,12 +29,13 @@ struct LinearGradArgs {
   void* dx;               // [M, K] bf16 or null
   void* dw;               // [N, K] bf16 or null
   float* dbias;           // [N] or null
-  char* scratch;
+  char* scratch;          // linear_scratch_bytes() behind the status block
   Status* status;
 };
 
-// Workspace past the status block, for the forward and the backward call.
-size_t linear_scratch_bytes(int M, int N, int K, int in_type);
+// Workspace of the backward call past the status block (dpre and partial column
+// sums; with bf16 operands only).
+size_t linear_scratch_bytes(int M, int N, int in_type);
 cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s);
 cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s);
 

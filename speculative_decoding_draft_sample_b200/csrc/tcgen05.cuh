@@ -85,6 +85,9 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 // Arrival without release: it orders no stores (a release here would wait for
 // the epilogue's stores to memory). Reads of tensor memory before it are
 // complete by tcgen05.wait::ld.
@@ -117,11 +120,12 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Arrives on b in both CTAs once every MMA issued before has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* b) {
+// Arrives on b in both CTAs of the pair (mask: their ranks) once every MMA issued
+// before has completed.
+__device__ __forceinline__ void mma_commit(uint64_t* b, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(b)),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
