@@ -574,18 +574,23 @@ struct Plan {
 };
 
 // The column width and the number of parts with the least time by measured costs
-// (ns at K = 1024 and 2048, 74 pairs): a block of the contraction takes 150 up to
-// 80 columns (the issuing loop), then 1.5 a column; a tile at least its epilogue;
-// the first loads and the last epilogue are not hidden; a joined tile has two
-// cluster barriers and the parts' sums on top.
+// in ns: a block of the contraction by its width (74 pairs, m1024 n18944, k2048
+// against k1024; up to 64 columns the issuing loop bounds it); a tile at least its
+// epilogue; the first loads and the last epilogue are not hidden; a joined tile has
+// two cluster barriers and the parts' sums on top. Clusters of 2, 4, 8 and 16 CTAs
+// of this size run 74, 33, 15 and 7 at once.
 Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
   constexpr int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};
+  constexpr double kBlockNs[] = {150, 150, 150, 150, 193, 221, 253, 294, 354, 408};
+  constexpr int kAtOnce[] = {kPlanPairs, 33, 15, 7};
   Plan best = {};
   double best_cost = 1e300;
-  for (int nt : kWidths) {
+  for (int i = 0; i < 10; ++i) {
+    const int nt = kWidths[i];
     if (b_cols && nt % 128 != 0) continue;
-    const double block = fmax(150.0, 20.0 + 1.5 * nt), epilogue = 600.0 + 9.5 * nt;
-    for (int parts = 1; parts <= 8; parts *= 2) {
+    const double block = kBlockNs[i], epilogue = 600.0 + 9.5 * nt;
+    for (int j = 0; j < 4; ++j) {
+      const int parts = 1 << j, at_once = kAtOnce[j];
       const int slots = (nt + kChunk - 1) / kChunk * kChunk * kLanes * 4;
       if (parts > 1 && (parts > kblocks || (parts - 1) * slots > kRing)) break;
       Plan p;
@@ -593,7 +598,7 @@ Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
       p.tiles_f = (int)((F + kTileF - 1) / kTileF);
       p.tiles_t = (int)((T + nt - 1) / nt);
       p.parts = parts;
-      const int tiles = p.tiles_f * p.tiles_t, at_once = kPlanPairs / parts;
+      const int tiles = p.tiles_f * p.tiles_t;
       if (parts > 1 && tiles > at_once) break;
       p.clusters = min(tiles, at_once);
       const double tile = (double)((kblocks + parts - 1) / parts) * block + 400.0;
