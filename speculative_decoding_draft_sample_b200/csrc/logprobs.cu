@@ -7,18 +7,26 @@
 //   logp(v) = (l_v - M) / temp - ln s,  H = ln s - ln(2) t / s,
 // one pass with a running maximum (s and t are rescaled when it grows:
 // s' = f s, t' = f (t + d s) with d = z of the old maximum, f = 2^d).
-// z is formed as a difference first, so that a row masked with the type's
-// lowest value (whose product with log2(e) / temp may overflow) keeps its
-// meaning, and clamped at -150 (2^z flushes to zero there), so that masked
-// entries add 0 * -150, not 0 * -inf.
+//
+// The pass is bound by instructions before it is bound by memory (bf16: 22
+// entries a nanosecond and SM at the copy rate), so an entry costs about five:
+// maxima and the clamp below on packed bf16 pairs, differences, products and sums
+// on packed fp32 pairs, one 2^z. z is formed as a difference first (its product
+// with the temperature cannot overflow for two finite neighbours), and logits are
+// clamped at M - 200 temp / log2(e), rounded down: 2^z is zero there, and masked
+// entries (-inf or the type's lowest value) add 0 * finite, never 0 * inf. Rows
+// whose maximum is itself of the size of the type's lowest value take a plain
+// second pass.
 //
 // Alternatives: a thread reads a fixed column of the row's 16-byte vectors and
 // knows its column's largest entry. The n largest entries of the slice all lie
-// in the n columns with the largest maxima, at or above the n-th of those
-// maxima, so only these columns are read a second time (n / 256 of the slice,
-// out of L2) and the few entries that pass are ranked by counting. Entries are
-// compared as 64-bit keys (value, then lowest index), which are unique, so
-// neither ties nor the order of the list's atomics change a result.
+// in the columns with the n largest maxima, at or above the n-th of those maxima.
+// One warp finds a value that n to n + 8 maxima reach by bisection; only these
+// columns are read a second time (out of L2) and the few entries that pass are
+// ranked by counting. Where equal maxima leave more than n + 8, the columns are
+// chosen by 64-bit keys (value, then lowest index). Candidates are always ranked
+// by these keys, which are unique, so neither ties nor the order of the list's
+// atomics change a result.
 #include <cooperative_groups.h>
 
 #include "logprobs.cuh"
@@ -29,19 +37,35 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;       // 16-byte loads in flight per thread
+enum : unsigned int {  // wait sites recorded when a bounded wait gives up
+  kWhereEmpty = 50,
+  kWhereFull = 51,
+};
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+constexpr int kThreads = 256;      // readers; one more warp feeds them
+constexpr int kUnroll = 4;       // 16-byte vectors of a thread in a ring slot
+constexpr int kSlotVecs = kUnroll * kThreads;
+constexpr int kSlots = 3;        // ring of 16 KB slots: with three CTAs on an SM up to 144 KB are on their way
+constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 8;   // CTAs that share a row
 constexpr int kCand = 1024;      // candidate list; a slice with more takes the selection loop
+constexpr int kSlack = 8;        // columns that the bisection may take beyond n
 constexpr float kFloorZ = -150.f;
+constexpr float kClampZ = 200.f;
+constexpr float kPlainMax = 1.0e37f;  // past this maximum (or its z) the plain pass
+constexpr float kMaxTemp = 1.0e30f;   // past this a temperature is an error
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // Order-preserving key of (value, index): larger value first, then lower index.
 // Zero is below every key. -0 and +0 are equal.
-__device__ __forceinline__ unsigned long long entry_key(float v, int idx) {
+__device__ __forceinline__ uint32_t value_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return ((unsigned long long)o << 32) | (uint32_t)~idx;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long entry_key(float v, int idx) {
+  return ((unsigned long long)value_key(v) << 32) | (uint32_t)~idx;
 }
 __device__ __forceinline__ int key_index(unsigned long long k) { return (int)~(uint32_t)k; }
 __device__ __forceinline__ float key_value(unsigned long long k) {
@@ -72,6 +96,9 @@ __device__ __forceinline__ RowStat stat_merge(const RowStat& a, const RowStat& b
   return r;
 }
 
+// Barrier of the eight reading warps.
+__device__ __forceinline__ void readers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 __device__ __forceinline__ unsigned long long block_max_key(unsigned long long k, unsigned long long* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -80,38 +107,174 @@ __device__ __forceinline__ unsigned long long block_max_key(unsigned long long k
     k = k2 > k ? k2 : k;
   }
   if (lane == 0) red[warp] = k;
-  __syncthreads();
+  readers_sync();
   unsigned long long best = red[0];
 #pragma unroll
   for (int w = 1; w < kThreads / 32; ++w) best = red[w] > best ? red[w] : best;
-  __syncthreads();
+  readers_sync();
   return best;
 }
 
+// Two fp32 values in one 64-bit register pair, and arithmetic on both at once.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A 16-byte vector as four 32-bit words: two bf16 entries or one fp32 entry each.
+template <int DT>
+struct Words;
+template <>
+struct Words<DSPARK_BF16> {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  __device__ __forceinline__ static uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ static uint32_t max_num(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ static float top(uint32_t w) {
+    return dspark::max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  // the largest value of the type not above v, in both halves (finite)
+  __device__ __forceinline__ static uint32_t floor_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    uint32_t h = u >> 16;
+    if ((u & 0x80000000u) && (u & 0xffffu)) ++h;
+    if (h > 0xff7fu) h = 0xff7fu;
+    return h | (h << 16);
+  }
+  // the entry pairs of a vector
+  __device__ __forceinline__ static f32x2 pair(const uint32_t* w, int i) {
+    return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+};
+template <>
+struct Words<DSPARK_F32> {
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  __device__ __forceinline__ static uint32_t max_nan(uint32_t a, uint32_t b) {
+    return __float_as_uint(dspark::max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ __forceinline__ static uint32_t max_num(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ __forceinline__ static float top(uint32_t w) { return __uint_as_float(w); }
+  __device__ __forceinline__ static uint32_t floor_of(float v) { return __float_as_uint(fmaxf(v, -3.4028234663852886e38f)); }
+  __device__ __forceinline__ static f32x2 pair(const uint32_t* w, int i) {
+    return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+};
+
 struct Shared {
+  uint4 ring[kSlots][kSlotVecs];
+  unsigned long long full[kSlots], empty[kSlots];    // mbarriers
   RowStat warp_stat[kThreads / 32];
   RowStat cta_stat[kMaxCluster];                     // CTA 0: every CTA's statistics
   unsigned long long lists[kMaxCluster * kMaxTop];   // CTA 0: every CTA's n largest keys
-  unsigned long long keys[kThreads];                 // the columns' largest keys
+  uint32_t vals[kThreads];                           // the columns' largest values (value_key), 0 = no entry
+  unsigned long long keys[kThreads];                 // the same as full keys, where values tie
   unsigned long long cand[kCand];
   unsigned long long red[kThreads / 32];
-  unsigned long long thr;                            // key of the n-th column maximum (0: fewer columns)
-  int sel[kMaxTop];                                  // the columns with the n largest maxima
+  unsigned long long thr;                            // the bound
+  int sel[kMaxTop + kSlack];                         // the columns that reach it
   int nsel, ncand;
+  int ties;                                          // equal maxima left too many columns
+  int dead;                                          // a bounded wait gave up
 };
 
-// The n largest keys of this CTA's slice [v0, v1) (vectors), descending, into
-// list[0..n) (zeros behind the last entry).
+// By one warp: a bound that at least n and at most n + kSlack of 256 keys reach
+// (all nonzero ones when there are no more than that); false when equal keys make
+// that impossible.
+template <typename Key>
+__device__ __forceinline__ bool bisect(const Key* keys, int n, int lane, Key lo, Key hi, Key* bound) {
+  constexpr int kPer = kThreads / 32;
+  Key k[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) k[j] = keys[j * 32 + lane];
+  auto reach = [&](Key b) {
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) c += k[j] >= b;
+    return (int)__reduce_add_sync(0xffffffffu, c);
+  };
+  int c = reach(lo);  // invariant: at least n reach lo (or all do), fewer than n reach hi + 1
+  while (c > n + kSlack && lo < hi) {
+    const Key mid = lo + (hi - lo) / 2 + 1;  // lo < mid <= hi
+    const int cm = reach(mid);
+    if (cm >= n) {
+      lo = mid;
+      c = cm;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  *bound = lo;
+  return c <= n + kSlack;
+}
+
+// The columns whose key reaches the bound.
+template <typename Key>
+__device__ __forceinline__ void list_columns(Shared& sh, const Key* keys, Key bound, int lane) {
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < kThreads / 32; ++j) {
+    const bool in = keys[j * 32 + lane] >= bound;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (in) sh.sel[at + __popc(m & ((1u << lane) - 1u))] = j * 32 + lane;
+    at += __popc(m);
+  }
+  if (lane == 0) sh.nsel = at;
+}
+
+__device__ void select_columns(Shared& sh, int n, int lane) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kThreads / 32; ++j) top = max(top, sh.vals[j * 32 + lane]);
+  // 32 of the maxima, one a lane, reach the least of the lanes' largest
+  const uint32_t lo = max(1u, __reduce_min_sync(0xffffffffu, top)), hi = max(lo, __reduce_max_sync(0xffffffffu, top));
+  uint32_t bound;
+  const bool ok = bisect<uint32_t>(sh.vals, n, lane, lo, hi, &bound);
+  if (ok) list_columns<uint32_t>(sh, sh.vals, bound, lane);
+  if (lane == 0) {
+    sh.thr = (unsigned long long)bound << 32;
+    sh.ties = !ok;
+    sh.ncand = 0;
+  }
+}
+
+// The entries of this CTA's slice [v0, v1) (vectors) that may be among its n
+// largest, in sh.cand (sh.ncand of them; more than kCand where the list is full).
 template <int DT>
-__device__ void slice_top(Shared& sh, const char* row, int v0, int v1, float mv, int mi, int n,
-                          unsigned long long* list) {
+__device__ void slice_candidates(Shared& sh, const char* row, int v0, int v1, float mv, int mi, int n) {
   constexpr int N = Vec16<DT>::N;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned long long key = 0;
-  if (v0 + tid < v1) {  // the first entry equal to the maximum, in the batch where it appeared
-    for (int j = 0; j < kUnroll && !key; ++j) {
+  if (sh.ties) {  // full keys: the first entry equal to the maximum, in the slot where it appeared
+    unsigned long long key = 0;
+    for (int j = kUnroll - 1; j >= 0; --j) {
       const int i = mi + j * kThreads;
-      if (i < v1) {
+      if (v0 + tid < v1 && i < v1) {
         float v[N];
         Vec16<DT>::load(row + (size_t)i * 16, v);
 #pragma unroll
@@ -119,54 +282,70 @@ __device__ void slice_top(Shared& sh, const char* row, int v0, int v1, float mv,
           if (v[e] == mv) key = entry_key(v[e], i * N + e);
       }
     }
+    sh.keys[tid] = key;
+    readers_sync();
+    if (warp == 0) {
+      const unsigned long long bound_value = sh.thr;
+      unsigned long long bound;
+      bisect<unsigned long long>(sh.keys, n, lane, bound_value, ~0ull, &bound);
+      list_columns<unsigned long long>(sh, sh.keys, bound, lane);
+      if (lane == 0) sh.thr = bound;
+    }
+    readers_sync();
   }
-  sh.keys[tid] = key;
-  if (tid == 0) {
-    sh.thr = 0;
-    sh.nsel = 0;
-    sh.ncand = 0;
-  }
-  if (tid < n) list[tid] = 0;
-  __syncthreads();
-  int rank = 0;
-  for (int j = 0; j < kThreads; ++j) rank += sh.keys[j] > key;
-  if (key && rank < n) {
-    sh.sel[rank] = tid;
-    atomicAdd(&sh.nsel, 1);
-    if (rank == n - 1) sh.thr = key;
-  }
-  __syncthreads();
-  const int nsel = sh.nsel;
   const unsigned long long thr = sh.thr;
-  for (int c = warp; c < nsel; c += kThreads / 32) {
-    for (int i = v0 + sh.sel[c] + lane * kThreads; i < v1; i += 32 * kThreads) {
+  const float floor = key_value(thr);
+  const int per = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a column
+  const int total = sh.nsel * per;
+  for (int q0 = tid; q0 < total; q0 += 4 * kThreads) {
+    uint4 w[4];
+    int at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int q = q0 + j * kThreads;
+      at[j] = v1;
+      if (q < total) at[j] = v0 + sh.sel[q / per] + (q % per) * kThreads;
+      if (at[j] < v1) w[j] = *reinterpret_cast<const uint4*>(row + (size_t)at[j] * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (at[j] >= v1) continue;
       float v[N];
-      Vec16<DT>::load(row + (size_t)i * 16, v);
+      Vec16<DT>::load(&w[j], v);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const unsigned long long k = entry_key(v[e], i * N + e);
-        if (k >= thr) {
-          const int at = atomicAdd(&sh.ncand, 1);
-          if (at < kCand) sh.cand[at] = k;
+        if (!(v[e] < floor)) {  // a bound below every value decodes to NaN
+          const unsigned long long k = entry_key(v[e], at[j] * N + e);
+          if (k >= thr) {
+            const int c = atomicAdd(&sh.ncand, 1);
+            if (c < kCand) sh.cand[c] = k;
+          }
         }
       }
     }
   }
-  __syncthreads();
+  readers_sync();
+}
+
+// Calls put(rank, key) for the n largest keys of the slice.
+template <int DT, typename Put>
+__device__ __forceinline__ void slice_top(Shared& sh, const char* row, int v0, int v1, int n, Put put) {
+  constexpr int N = Vec16<DT>::N;
+  const int tid = threadIdx.x;
   const int cnt = sh.ncand;
   if (cnt <= kCand) {
     for (int c = tid; c < cnt; c += kThreads) {
       const unsigned long long k = sh.cand[c];
       int r = 0;
       for (int j = 0; j < cnt && r < n; ++j) r += sh.cand[j] > k;
-      if (r < n) list[r] = k;
+      if (r < n) put(r, k);
     }
-  } else {  // very many entries above the threshold: one at a time, largest first
-    const int per = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a column
+  } else {  // very many entries above the bound: one at a time, largest first
+    const int per = (v1 - v0 + kThreads - 1) / kThreads;
     unsigned long long last = ~0ull;
     for (int r = 0; r < n; ++r) {
       unsigned long long best = 0;
-      for (int q = tid; q < nsel * per; q += kThreads) {
+      for (int q = tid; q < sh.nsel * per; q += kThreads) {
         const int i = v0 + sh.sel[q / per] + (q % per) * kThreads;
         if (i >= v1) continue;
         float v[N];
@@ -178,17 +357,46 @@ __device__ void slice_top(Shared& sh, const char* row, int v0, int v1, float mv,
         }
       }
       last = block_max_key(best, sh.red);
-      if (tid == 0) list[r] = last;
       if (!last) break;
+      if (tid == 0) put(r, last);
     }
   }
-  __syncthreads();
+}
+
+// s and t of a whole row whose maximum m is known, entry by entry in the plain
+// form (rows whose maximum is of the size of the type's lowest value).
+template <int DT>
+__device__ void plain_sums(Shared& sh, const char* row, int nvec, float cs, RowStat& c) {
+  constexpr int N = Vec16<DT>::N;
+  float s = 0.f, t = 0.f;
+  for (int i = threadIdx.x; i < nvec; i += kThreads) {
+    float v[N];
+    Vec16<DT>::load(row + (size_t)i * 16, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float z = v[e] == -INFINITY ? kFloorZ : zdiff(v[e], c.m, cs);
+      const float w = ex2(z);
+      s += w;
+      t = fmaf(w, z, t);
+    }
+  }
+  s = warp_sum(s);
+  t = warp_sum(t);
+  readers_sync();
+  if ((threadIdx.x & 31) == 0) sh.warp_stat[threadIdx.x >> 5] = {c.m, s, t, c.chk};
+  readers_sync();
+  c.s = c.t = 0.f;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    c.s += sh.warp_stat[w].s;
+    c.t += sh.warp_stat[w].t;
+  }
 }
 
 // A cluster of C CTAs takes a row; CTA q reads vectors [q per, (q + 1) per).
 template <int DT>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a, int C) {
-  __shared__ Shared sh;
+__global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(LogprobArgs a, int C) {
+  extern __shared__ __align__(128) unsigned char shared_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(shared_raw);
   constexpr int N = Vec16<DT>::N;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long r = blockIdx.x / C;
@@ -196,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a, int C
   const int b = (int)(r / a.J);
   const int tok = a.tok[r], n = a.n_top;
   const float tau = a.temp ? a.temp[b] : 1.f;
-  const bool bad_tok = tok < -1 || tok >= a.V, bad_temp = !(tau >= 0.f);
+  const bool bad_tok = tok < -1 || tok >= a.V, bad_temp = !(tau >= 0.f && tau <= kMaxTemp);
   if (tok < 0 || bad_tok || bad_temp) {  // nothing of the row is read
     if (q == 0) {
       if (tid == 0) {
@@ -219,92 +427,186 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a, int C
   const int nvec = a.V / N, per = (nvec + C - 1) / C;
   const int v0 = q * per, v1 = min(nvec, v0 + per);
 
-  RowStat st = {-INFINITY, 0.f, 0.f, -INFINITY};
-  int mi = v0 + tid;
-  for (int i = v0 + tid; i < v1; i += kUnroll * kThreads) {
-    float v[kUnroll][N];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      if (i + j * kThreads < v1) {
-        Vec16<DT>::load(row + (size_t)(i + j * kThreads) * 16, v[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[j][e] = -INFINITY;
+  // The slice comes in slots of 16 KB, copied by the bulk-copy engine while the
+  // readers work on the slots before. The feeding warp prepares the barriers and
+  // starts at once.
+  const int chunks = (max(0, v1 - v0) + kSlotVecs - 1) / kSlotVecs;
+  if (warp == kThreads / 32) {
+    bool ok = true;
+    int issued = 0;
+    auto issue = [&](int c) {
+      const int slot = c % kSlots, first = v0 + c * kSlotVecs, bytes = min(kSlotVecs, v1 - first) * 16;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(&sh.full[slot])), "r"(bytes) : "memory");
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(saddr(sh.ring[slot])),
+          "l"(row + (size_t)first * 16), "r"(bytes), "r"(saddr(&sh.full[slot]))
+          : "memory");
+      ++issued;
+    };
+    if (lane == 0) {
+      for (int i = 0; i < kSlots; ++i) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&sh.full[i])) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(&sh.empty[i])), "r"(kThreads / 32) : "memory");
+      }
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      sh.dead = 0;
+      for (int c = 0; c < min(chunks, kSlots); ++c) issue(c);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      for (int c = kSlots; c < chunks; ++c) {
+        ok = mbar_wait_bounded(saddr(&sh.empty[c % kSlots]), (c / kSlots - 1) & 1);
+        if (!ok) break;
+        issue(c);
+      }
+      if (!ok) {
+        report_wait(a.status, kWhereEmpty, b);
+        *(volatile int*)&sh.dead = 1;
+        for (int c = max(0, issued - kSlots); c < issued; ++c)  // let issued copies land before the CTA exits
+          mbar_wait_bounded(saddr(&sh.full[c % kSlots]), (c / kSlots) & 1);
       }
     }
-    float bm = v[0][0];
+    __syncwarp();
+  } else {
+    __syncthreads();
+  }
+
+  using W = Words<DT>;
+  constexpr int kPairs = N / 2;
+  RowStat st = {-INFINITY, 0.f, 0.f, -INFINITY};
+  const float reach = kClampZ / cs;
+  const f32x2 cs2 = pack2(cs, cs);
+  f32x2 neg_m = 0, s2[2] = {0, 0}, t2[2] = {0, 0};  // minus the maximum (0 while it is -inf); sums of both halves
+  uint32_t low = W::floor_of(-reach);
+  int mi = v0 + tid;
+  const int todo = warp < kThreads / 32 ? chunks : 0;
+  for (int c = 0; c < todo; ++c) {
+    const int slot = c % kSlots, i = v0 + c * kSlotVecs + tid;
+    const bool arrived = !*(volatile int*)&sh.dead && mbar_wait_bounded(saddr(&sh.full[slot]), (c / kSlots) & 1);
+    if (!__all_sync(0xffffffffu, arrived)) {
+      if (lane == 0 && !*(volatile int*)&sh.dead) report_wait(a.status, kWhereFull, b);
+      *(volatile int*)&sh.dead = 1;
+      break;
+    }
+    uint32_t v[kUnroll][4];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      uint4 q = make_uint4(W::kNegInf, W::kNegInf, W::kNegInf, W::kNegInf);
+      if (i + j * kThreads < v1) q = sh.ring[slot][tid + j * kThreads];
+      v[j][0] = q.x;
+      v[j][1] = q.y;
+      v[j][2] = q.z;
+      v[j][3] = q.w;
+    }
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&sh.empty[slot])) : "memory");
+    uint32_t b2 = v[0][0];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
-      for (int e = 0; e < N; ++e) bm = max_nan(bm, v[j][e]);
+      for (int e = 0; e < 4; ++e) b2 = W::max_nan(b2, v[j][e]);
+    const float bm = W::top(b2);
     st.chk = max_nan(st.chk, bm);
     if (bm > st.m) {
       const float d = zdiff(st.m, bm, cs), f = ex2(d);
-      st.t = f * fmaf(d, st.s, st.t);
-      st.s *= f;
+      const f32x2 d2 = pack2(d, d), f2 = pack2(f, f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        t2[e] = mul2(f2, fma2(d2, s2[e], t2[e]));
+        s2[e] = mul2(f2, s2[e]);
+      }
       st.m = bm;
       mi = i;
+      neg_m = pack2(-bm, -bm);
+      low = W::floor_of(__fsub_rd(bm, reach));
     }
-    const float mz = st.m == -INFINITY ? 0.f : st.m;
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
+    for (int j = 0; j < kUnroll; ++j) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float z = fmaxf((v[j][e] - mz) * cs, kFloorZ);
-        const float w = ex2(z);
-        st.s += w;
-        st.t = fmaf(w, z, st.t);
+      for (int e = 0; e < 4; ++e) v[j][e] = W::max_num(v[j][e], low);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        const f32x2 z2 = mul2(add2(W::pair(v[j], e), neg_m), cs2);
+        float za, zb;
+        unpack2(z2, za, zb);
+        const f32x2 w2 = pack2(ex2(za), ex2(zb));
+        s2[e & 1] = add2(s2[e & 1], w2);
+        t2[e & 1] = fma2(w2, z2, t2[e & 1]);
       }
+    }
   }
-  const float mv = st.m;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    RowStat p;
-    p.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    p.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    p.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-    p.chk = __shfl_xor_sync(0xffffffffu, st.chk, o);
-    st = stat_merge(st, p, cs);
+  {
+    float a0, a1, b0, b1;
+    unpack2(add2(s2[0], s2[1]), a0, a1);
+    unpack2(add2(t2[0], t2[1]), b0, b1);
+    st.s = a0 + a1;
+    st.t = b0 + b1;
   }
-  if (lane == 0) sh.warp_stat[warp] = st;
-  __syncthreads();
-
   cg::cluster_group cluster = cg::this_cluster();
   if (C > 1) cluster.sync();  // CTA 0's shared memory exists before it is written
   Shared* root = C > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
-  if (tid == 0) {
-    RowStat c = sh.warp_stat[0];
-    for (int w = 1; w < kThreads / 32; ++w) c = stat_merge(c, sh.warp_stat[w], cs);
-    root->cta_stat[q] = c;
+  const bool reader = warp < kThreads / 32;
+  const int mv_i = mi;
+  const float mv = st.m;
+  if (reader) {
+    if (n) sh.vals[tid] = v0 + tid < v1 ? value_key(mv) : 0;
+    if (n && tid < n) root->lists[q * n + tid] = 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      RowStat p;
+      p.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+      p.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+      p.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+      p.chk = __shfl_xor_sync(0xffffffffu, st.chk, o);
+      st = stat_merge(st, p, cs);
+    }
+    if (lane == 0) sh.warp_stat[warp] = st;
+    readers_sync();
+    if (warp == 0 && n) select_columns(sh, n, lane);
+    if (warp == 1 && lane == 0) {
+      RowStat c = sh.warp_stat[0];
+      for (int w = 1; w < kThreads / 32; ++w) c = stat_merge(c, sh.warp_stat[w], cs);
+      root->cta_stat[q] = c;
+    }
+    readers_sync();
+    if (n) slice_candidates<DT>(sh, row, v0, v1, mv, mv_i, n);
+    if (n && C > 1) slice_top<DT>(sh, row, v0, v1, n, [&](int rank, unsigned long long k) { root->lists[q * n + rank] = k; });
   }
-  if (n) slice_top<DT>(sh, row, v0, v1, mv, mi, n, root->lists + q * n);
   if (C > 1) cluster.sync();
-  if (q != 0) return;
-  __syncthreads();
+  if (q != 0 || !reader) return;
 
   RowStat c = sh.cta_stat[0];
   for (int w = 1; w < C; ++w) c = stat_merge(c, sh.cta_stat[w], cs);
-  const bool bad = c.chk != c.chk || c.m == INFINITY || c.m == -INFINITY;
+  const bool bad = c.chk != c.chk || c.m == INFINITY || c.m == -INFINITY || sh.dead;
+  if (!bad && !(fabsf(c.m) < kPlainMax && fabsf(c.m) * cs < kPlainMax)) plain_sums<DT>(sh, row, nvec, cs, c);
   const float ln_s = logf(c.s);
   if (tid == 0) {
-    if (bad) report(a.status, DSPARK_STATUS_BAD_ROW, b);
+    if (bad && !sh.dead) report(a.status, DSPARK_STATUS_BAD_ROW, b);
     const float l = Elem<DT>::load(reinterpret_cast<const typename Elem<DT>::T*>(row), tok);
     a.logp[r] = bad ? 0.f : (l - c.m) / temp - ln_s;
     if (a.entropy) a.entropy[r] = bad ? 0.f : fmaxf(0.f, ln_s - kLn2 * (c.t / c.s));
     if (a.lse) a.lse[r] = bad ? 0.f : c.m / temp + ln_s;
   }
-  for (int k = tid; k < C * n; k += kThreads) {
-    const unsigned long long key = sh.lists[k];
-    int rank = 0;
-    for (int j = 0; j < C * n; ++j) rank += sh.lists[j] > key;
-    if (!bad && key && rank < n) {
-      a.top_idx[r * n + rank] = key_index(key);
-      a.top_logp[r * n + rank] = (key_value(key) - c.m) / temp - ln_s;
+  if (bad) {
+    if (tid < n) {
+      a.top_idx[r * n + tid] = -1;
+      a.top_logp[r * n + tid] = -INFINITY;
     }
+    return;
   }
-  if (bad && tid < n) {
-    a.top_idx[r * n + tid] = -1;
-    a.top_logp[r * n + tid] = -INFINITY;
+  auto put = [&](int rank, unsigned long long key) {
+    a.top_idx[r * n + rank] = key_index(key);
+    a.top_logp[r * n + rank] = (key_value(key) - c.m) / temp - ln_s;
+  };
+  if (C == 1) {
+    if (n) slice_top<DT>(sh, row, v0, v1, n, put);
+  } else {
+    for (int k = tid; k < C * n; k += kThreads) {
+      const unsigned long long key = sh.lists[k];
+      int rank = 0;
+      for (int j = 0; j < C * n; ++j) rank += sh.lists[j] > key;
+      if (key && rank < n) put(rank, key);
+    }
   }
 }
 
@@ -326,7 +628,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
     const int tok = a.tok[r];
     const float tau = a.temp ? a.temp[b] : 1.f;
     const float lse = a.lse[r];
-    const bool bad_tok = tok < -1 || tok >= a.V, bad_temp = !(tau >= 0.f);
+    const bool bad_tok = tok < -1 || tok >= a.V, bad_temp = !(tau >= 0.f && tau <= kMaxTemp);
     const bool bad_row = !(fabsf(lse) < INFINITY);
     const bool skip = tok < 0 || bad_tok || bad_temp || bad_row;
     if (tok != -1 && skip && seg == 0 && threadIdx.x == 0)
@@ -373,8 +675,11 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int num_sms, cudaStream_t s) {
   auto kern = a.dtype == DSPARK_F32 ? logprobs_kernel<DSPARK_F32> : logprobs_kernel<DSPARK_BF16>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads + 32);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = s;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
