@@ -11,12 +11,12 @@
 // The pass is bound by instructions before it is bound by memory (bf16: 22
 // entries a nanosecond and SM at the copy rate), so an entry costs about five:
 // maxima and the clamp below on packed bf16 pairs, differences, products and sums
-// on packed fp32 pairs, one 2^z. z is formed as a difference first (its product
-// with the temperature cannot overflow for two finite neighbours), and logits are
-// clamped at M - 200 temp / log2(e), rounded down: 2^z is zero there, and masked
-// entries (-inf or the type's lowest value) add 0 * finite, never 0 * inf. Rows
-// whose maximum is itself of the size of the type's lowest value take a plain
-// second pass.
+// on packed fp32 pairs, one 2^z. z = l cs - round(M cs) is one fused product (cs =
+// log2(e) / temp); the rounding of M cs is known and taken out of the thread's sums
+// at the end. Logits are clamped at M - 200 / cs, rounded down: 2^z is zero there,
+// and masked entries (-inf or the type's lowest value) add 0 * finite, never
+// 0 * inf. Rows whose maximum is itself of the size of the type's lowest value take
+// a plain second pass.
 //
 // Alternatives: a thread reads a fixed column of the row's 16-byte vectors and
 // knows its column's largest entry. The n largest entries of the slice all lie
@@ -476,30 +476,13 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   RowStat st = {-INFINITY, 0.f, 0.f, -INFINITY};
   const float reach = kClampZ / cs;
   const f32x2 cs2 = pack2(cs, cs);
-  f32x2 neg_m = 0, s2[2] = {0, 0}, t2[2] = {0, 0};  // minus the maximum (0 while it is -inf); sums of both halves
+  float mz = 0.f;                                        // the maximum's z, rounded
+  bool scaled = false;                                   // the sums are those of mz (else nothing is in them)
+  f32x2 neg_mz = 0, s2[2] = {0, 0}, t2[2] = {0, 0};      // sums of 2^z', z' 2^z' with z' = l cs - mz, both halves
   uint32_t low = W::floor_of(-reach);
   int mi = v0 + tid;
-  const int todo = warp < kThreads / 32 ? chunks : 0;
-  for (int c = 0; c < todo; ++c) {
-    const int slot = c % kSlots, i = v0 + c * kSlotVecs + tid;
-    const bool arrived = !*(volatile int*)&sh.dead && mbar_wait_bounded(saddr(&sh.full[slot]), (c / kSlots) & 1);
-    if (!__all_sync(0xffffffffu, arrived)) {
-      if (lane == 0 && !*(volatile int*)&sh.dead) report_wait(a.status, kWhereFull, b);
-      *(volatile int*)&sh.dead = 1;
-      break;
-    }
-    uint32_t v[kUnroll][4];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      uint4 q = make_uint4(W::kNegInf, W::kNegInf, W::kNegInf, W::kNegInf);
-      if (i + j * kThreads < v1) q = sh.ring[slot][tid + j * kThreads];
-      v[j][0] = q.x;
-      v[j][1] = q.y;
-      v[j][2] = q.z;
-      v[j][3] = q.w;
-    }
-    __syncwarp();
-    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&sh.empty[slot])) : "memory");
+
+  auto batch = [&](uint32_t (&v)[kUnroll][4], int i) {
     uint32_t b2 = v[0][0];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
@@ -508,7 +491,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
     const float bm = W::top(b2);
     st.chk = max_nan(st.chk, bm);
     if (bm > st.m) {
-      const float d = zdiff(st.m, bm, cs), f = ex2(d);
+      // a maximum of the size of the type's lowest value adds nothing here: another
+      // column's is larger, or the row takes the plain pass
+      const bool fits = fabsf(bm) * cs < kPlainMax;
+      const float bz = fits ? bm * cs : 0.f, d = fmaxf(scaled ? mz - bz : kFloorZ, kFloorZ), f = ex2(d);
       const f32x2 d2 = pack2(d, d), f2 = pack2(f, f);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -517,8 +503,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
       }
       st.m = bm;
       mi = i;
-      neg_m = pack2(-bm, -bm);
-      low = W::floor_of(__fsub_rd(bm, reach));
+      mz = bz;
+      scaled = fits;
+      neg_mz = pack2(-bz, -bz);
+      low = W::floor_of(fits ? __fsub_rd(bm, reach) : -reach);
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
@@ -526,7 +514,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
       for (int e = 0; e < 4; ++e) v[j][e] = W::max_num(v[j][e], low);
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) {
-        const f32x2 z2 = mul2(add2(W::pair(v[j], e), neg_m), cs2);
+        const f32x2 z2 = fma2(W::pair(v[j], e), cs2, neg_mz);
         float za, zb;
         unpack2(z2, za, zb);
         const f32x2 w2 = pack2(ex2(za), ex2(zb));
@@ -534,14 +522,53 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
         t2[e & 1] = fma2(w2, z2, t2[e & 1]);
       }
     }
-  }
-  {
+  };
+
+  if (warp < kThreads / 32) {
+    int slot = 0, i = v0 + tid;
+    uint32_t ph = 0;
+    for (int c = 0; c < chunks; ++c, i += kSlotVecs) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(saddr(&sh.full[slot]), ph))) {
+        if (lane == 0 && !*(volatile int*)&sh.dead) report_wait(a.status, kWhereFull, b);
+        *(volatile int*)&sh.dead = 1;
+        break;
+      }
+      uint32_t v[kUnroll][4];
+      const uint4* src = &sh.ring[slot][tid];
+      auto take = [&](int j) {
+        const uint4 x = src[j * kThreads];
+        v[j][0] = x.x;
+        v[j][1] = x.y;
+        v[j][2] = x.z;
+        v[j][3] = x.w;
+      };
+      if (c + 1 < chunks) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) take(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          v[j][0] = v[j][1] = v[j][2] = v[j][3] = W::kNegInf;
+          if (i + j * kThreads < v1) take(j);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&sh.empty[slot])) : "memory");
+      batch(v, i);
+      if (++slot == kSlots) {
+        slot = 0;
+        ph ^= 1;
+      }
+    }
     float a0, a1, b0, b1;
     unpack2(add2(s2[0], s2[1]), a0, a1);
     unpack2(add2(t2[0], t2[1]), b0, b1);
-    st.s = a0 + a1;
-    st.t = b0 + b1;
+    // z' = z + e with e = m cs - mz, the rounding of mz
+    const float e = scaled ? fmaf(st.m, cs, -mz) : 0.f, f = ex2(-e);
+    st.s = f * (a0 + a1);
+    st.t = f * ((b0 + b1) - e * (a0 + a1));
   }
+
   cg::cluster_group cluster = cg::this_cluster();
   if (C > 1) cluster.sync();  // CTA 0's shared memory exists before it is written
   Shared* root = C > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
