@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cv
 constexpr int kThreads = 256;      // readers; one more warp feeds them
 constexpr int kUnroll = 4;       // 16-byte vectors of a thread in a ring slot
 constexpr int kSlotVecs = kUnroll * kThreads;
-constexpr int kSlots = 3;        // ring of 16 KB slots: with three CTAs on an SM up to 144 KB are on their way
-constexpr int kCtasPerSm = 3;
+constexpr int kSlots = 2;        // ring of 16 KB slots: with four CTAs on an SM up to 128 KB are on their way
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxCluster = 8;   // CTAs that share a row
 constexpr int kCand = 1024;      // candidate list; a slice with more takes the selection loop
 constexpr int kSlack = 8;        // columns that the bisection may take beyond n
@@ -483,12 +483,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   int mi = v0 + tid;
 
   auto batch = [&](uint32_t (&v)[kUnroll][4], int i) {
-    uint32_t b2 = v[0][0];
+    uint32_t b2[4];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b2 = W::max_nan(b2, v[j][e]);
-    const float bm = W::top(b2);
+    for (int e = 0; e < 4; ++e) b2[e] = W::max_nan(W::max_nan(v[0][e], v[1][e]), W::max_nan(v[2][e], v[3][e]));
+    const float bm = W::top(W::max_nan(W::max_nan(b2[0], b2[1]), W::max_nan(b2[2], b2[3])));
     st.chk = max_nan(st.chk, bm);
     if (bm > st.m) {
       // a maximum of the size of the type's lowest value adds nothing here: another
