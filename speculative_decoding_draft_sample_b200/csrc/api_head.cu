@@ -126,6 +126,7 @@ int dspark_residual_norm_grad(const void* s, const void* weight, const float* rs
   a.dx = dx;
   a.dweight = dweight;
   a.partial = reinterpret_cast<float*>(scratch_of(ws));
+  a.status = static_cast<Status*>(ws);
   return cuda_status(norm_grad_launch(a, (cudaStream_t)stream));
 }
 

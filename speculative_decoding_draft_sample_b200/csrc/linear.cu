@@ -521,34 +521,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dpre = round_bf16(dy act'(pre)) (the tensor cores take bf16 operands; the
 // rounding is half a bf16 step of each factor, as in the bf16 result) and
 // per-CTA column sums of the unrounded values. A CTA takes 256 columns and a
-// contiguous run of rows, 8 rows at a time.
-constexpr int kDpreRows = 8;
+// contiguous run of rows, a warp every eighth row, four of them in flight.
+constexpr int kDpreRows = 8, kDpreAhead = 4;
 
-__global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* pre, int M, int N, int act, int rows_per,
-                                                   void* dpre, float* partial) {
+template <int ACT>
+__global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* pre, int M, int N, int rows_per, void* dpre,
+                                                   float* partial) {
   __shared__ float part[kDpreRows][256 + 8];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int n0 = blockIdx.x * 256 + lane * 8;
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows_per);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (n0 < N) {
-    for (int m = blockIdx.y * rows_per + row; m < m1; m += kDpreRows) {
-      const size_t at = ((size_t)m * N + n0) * 2;
-      float d[8];
-      Vec16<DSPARK_BF16>::load(static_cast<const char*>(dy) + at, d);
-      if (act != DSPARK_ACT_NONE) {
-        float z[8];
-        Vec16<DSPARK_BF16>::load(static_cast<const char*>(pre) + at, z);
-        alignas(16) uint16_t o[8];
+    for (int m = blockIdx.y * rows_per + row; m < m1; m += kDpreRows * kDpreAhead) {
+      uint4 d4[kDpreAhead], z4[kDpreAhead];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[e] *= activate_grad(z[e], act);
-          o[e] = Elem<DSPARK_BF16>::store_round(d[e]);
+      for (int j = 0; j < kDpreAhead; ++j) {
+        const size_t at = ((size_t)(m + j * kDpreRows) * N + n0) * 2;
+        if (m + j * kDpreRows < m1) {
+          d4[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(dy) + at);
+          if (ACT != DSPARK_ACT_NONE) z4[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(pre) + at);
         }
-        *reinterpret_cast<uint4*>(static_cast<char*>(dpre) + at) = *reinterpret_cast<const uint4*>(o);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += d[e];
+      for (int j = 0; j < kDpreAhead; ++j) {
+        if (m + j * kDpreRows >= m1) continue;
+        float d[8];
+        Vec16<DSPARK_BF16>::load(&d4[j], d);
+        if (ACT != DSPARK_ACT_NONE) {
+          float z[8];
+          Vec16<DSPARK_BF16>::load(&z4[j], z);
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] *= activate_grad(z[e], ACT);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+          *reinterpret_cast<uint4*>(static_cast<char*>(dpre) + ((size_t)(m + j * kDpreRows) * N + n0) * 2) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += d[e];
+      }
     }
   }
   if (!partial) return;
@@ -621,10 +634,10 @@ Plan plan_forward(int M, int N, int K, int in_type) {
 Plan plan_dx(int M, int N, int K) { return make_plan(K, M, kblocks_of(N, 64), false); }
 Plan plan_dw(int M, int N, int K) { return make_plan(K, N, kblocks_of(M, 64), true); }
 
-// Row runs of dpre_kernel: enough CTAs for two on every SM, 64 rows or more each.
+// Row runs of dpre_kernel: enough CTAs for six on every SM, 32 rows or more each.
 inline int dpre_runs(int M, int N) {
   const int cols = (N + 255) / 256;
-  return max(1, min((M + 63) / 64, (4 * kPlanPairs + cols - 1) / cols));
+  return max(1, min((M + 31) / 32, (12 * kPlanPairs + cols - 1) / cols));
 }
 
 template <bool F8, bool A_MN, bool B_MN, bool STAGED>
@@ -696,8 +709,11 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   if (a.act != DSPARK_ACT_NONE || a.dbias) {
     const int runs = dpre_runs(a.M, a.N);
     const int rows_per = (a.M + runs - 1) / runs;
-    dpre_kernel<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, a.act, rows_per, dpre_buf,
-                                                              a.dbias ? partial : nullptr);
+    auto kern = a.act == DSPARK_ACT_RELU   ? dpre_kernel<DSPARK_ACT_RELU>
+                : a.act == DSPARK_ACT_SILU ? dpre_kernel<DSPARK_ACT_SILU>
+                : a.act == DSPARK_ACT_GELU ? dpre_kernel<DSPARK_ACT_GELU>
+                                           : dpre_kernel<DSPARK_ACT_NONE>;
+    kern<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, rows_per, dpre_buf, a.dbias ? partial : nullptr);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.dbias && (e = column_sums_launch(partial, runs, a.N, a.dbias, s)) != cudaSuccess) return e;

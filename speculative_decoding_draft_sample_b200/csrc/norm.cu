@@ -49,20 +49,21 @@ __device__ __forceinline__ void store_e4m3(void* p, const float* v) {
     *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-// Sum and NaN-propagating maximum over the block (red: 2 x 32 floats).
-__device__ __forceinline__ void block_sum_max(float& s, float& m, float* red) {
+// Sum and NaN-propagating maximum over the block (red: 2 x 32 floats); returns
+// whether any thread's flag is set. One block barrier: the caller alternates
+// between two buffers, so the next reduction's writes meet no late reader.
+__device__ __forceinline__ bool block_sum_max(float& s, float& m, float* red, bool flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  if (nw == 1) return;
   if (lane == 0) {
     red[warp] = s;
     red[32 + warp] = m;
   }
-  __syncthreads();
+  const bool any = __syncthreads_or(flag);
   s = lane < nw ? red[lane] : 0.f;
   m = lane < nw ? red[32 + lane] : 0.f;
 #pragma unroll
@@ -70,213 +71,319 @@ __device__ __forceinline__ void block_sum_max(float& s, float& m, float* red) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
+  return any;
 }
 
-// One CTA per row, NV 16-byte vectors per thread.
+enum : unsigned int { kWhereNormRow = 60 };  // wait site recorded when a bounded wait gives up
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+constexpr int kMaxStages = 4;
+
+// The rows blockIdx.x, blockIdx.x + gridDim.x, ... of up to three matrices, fed
+// through a ring of `stages` shared-memory rows. Row number it is read between
+// wait(it) and refill(it), the latter by every thread after a block barrier that
+// follows the reads.
+template <int ARRAYS>
+struct RowFeed {
+  unsigned char* ring;
+  unsigned long long* full;
+  const char* src[ARRAYS];
+  int stages, bytes, rows;
+
+  __device__ __forceinline__ void issue(int it) const {
+    const long long r = blockIdx.x + (long long)it * gridDim.x;
+    if (r >= rows) return;
+    const int st = it % stages;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < ARRAYS; ++k) n += src[k] != nullptr;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(full + st)), "r"(n * bytes) : "memory");
+#pragma unroll
+    for (int k = 0; k < ARRAYS; ++k)
+      if (src[k])
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                saddr(ring + (size_t)(st * ARRAYS + k) * bytes)),
+            "l"(src[k] + r * bytes), "r"(bytes), "r"(saddr(full + st))
+            : "memory");
+  }
+  __device__ __forceinline__ void start() const {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < stages; ++i)
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(full + i)) : "memory");
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      for (int i = 0; i < stages; ++i) issue(i);
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ bool wait(int it) const {
+    return mbar_wait_bounded(saddr(full + it % stages), (it / stages) & 1);
+  }
+  __device__ __forceinline__ const unsigned char* row(int it, int k) const {
+    return ring + (size_t)(it % stages * ARRAYS + k) * bytes;
+  }
+  __device__ __forceinline__ void refill(int it) const {
+    if (threadIdx.x == 0) issue(it + stages);
+  }
+  // after a wait for row `it` gave up: let the copies on their way land
+  __device__ __forceinline__ void drain(int it) const {
+    if (threadIdx.x == 0)
+      for (int i = it; i < it + stages; ++i)
+        if (blockIdx.x + (long long)i * gridDim.x < rows) wait(i);
+  }
+};
+
+// NV 16-byte vectors of a row per thread.
 template <int DT, bool E4M3, int NV>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
-  __shared__ float red[64];
+__global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) norm_kernel(NormArgs a, int stages) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[kMaxStages];
+  __shared__ float red[2][64];
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
   const int tid = threadIdx.x, T = blockDim.x, nvec = a.H / N;
-  const long long r = blockIdx.x;
-  const size_t off = (size_t)r * a.H * es;
-  const char* x = static_cast<const char*>(a.x) + off;
-  const char* delta = a.delta ? static_cast<const char*>(a.delta) + off : nullptr;
-  float v[NV][N];
+  const RowFeed<2> feed = {ring, full, {static_cast<const char*>(a.x), static_cast<const char*>(a.delta)}, stages, a.H * es, a.M};
+  feed.start();
   uint4 wr[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * T;
-    if (i < nvec) {
-      Vec16<DT>::load(x + (size_t)i * 16, v[j]);
-      wr[j] = load_raw(static_cast<const char*>(a.weight) + (size_t)i * 16);
-    }
-  }
-  if (delta) {
+  for (int j = 0; j < NV; ++j)
+    if (tid + j * T < nvec) wr[j] = load_raw(static_cast<const char*>(a.weight) + (size_t)(tid + j * T) * 16);
+  int it = 0;
+  for (long long r = blockIdx.x; r < a.M; r += gridDim.x, ++it) {
+    const bool arrived = feed.wait(it);
+    const size_t off = (size_t)r * a.H * es;
+    float v[NV][N];
+    float ss = 0.f, mx = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * T;
-      if (i < nvec) {
+      if (i >= nvec) continue;
+      Vec16<DT>::load(feed.row(it, 0) + i * 16, v[j]);
+      if (a.delta) {
         float d[N];
-        Vec16<DT>::load(delta + (size_t)i * 16, d);
+        Vec16<DT>::load(feed.row(it, 1) + i * 16, d);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[j][e] += d[e];
       }
-    }
-  }
-  float ss = 0.f, mx = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (tid + j * T < nvec) {
       float w[N];
-      unpack16<DT>(wr[j], w);
+      if (E4M3) unpack16<DT>(wr[j], w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         ss = fmaf(v[j][e], v[j][e], ss);
         if (E4M3) mx = max_nan(mx, fabsf(v[j][e] * w[e]));
       }
     }
-  block_sum_max(ss, mx, red);
-  // NaN or a sum of squares past fp32 makes the whole row NaN
-  const bool bad = !(ss < INFINITY) || (E4M3 && !(mx < INFINITY));
-  const float rstd = bad ? NAN : 1.f / sqrtf(ss / (float)a.H + a.eps);
-  float inv = 1.f;  // 1 / scale: finite, as the scale is a normal number
-  if (E4M3) {
-    const float scale = bad ? NAN : fmaxf(mx * rstd / kE4m3Max, kMinScale);
-    inv = 1.f / scale;
-    if (tid == 0) a.y_scale[r] = scale;
-  }
-  if (tid == 0) {
-    if (a.rstd) a.rstd[r] = rstd;
-    if (bad) report(a.status, DSPARK_STATUS_BAD_ROW, (int)r);
-  }
-  char* sum = a.sum ? static_cast<char*>(a.sum) + off : nullptr;
-  char* y = static_cast<char*>(a.y) + (E4M3 ? (size_t)r * a.H : off);
+    if (block_sum_max(ss, mx, red[it & 1], !arrived)) {  // a wait gave up
+      feed.drain(it);
+      if (tid == 0) report_wait(a.status, kWhereNormRow, (int)r);
+      return;
+    }
+    feed.refill(it);
+    // NaN or a sum of squares past fp32 makes the whole row NaN
+    const bool bad = !(ss < INFINITY) || (E4M3 && !(mx < INFINITY));
+    const float rstd = bad ? NAN : 1.f / sqrtf(ss / (float)a.H + a.eps);
+    float inv = 1.f;  // 1 / scale: finite, as the scale is a normal number
+    if (E4M3) {
+      const float scale = bad ? NAN : fmaxf(mx * rstd / kE4m3Max, kMinScale);
+      inv = 1.f / scale;
+      if (tid == 0) a.y_scale[r] = scale;
+    }
+    if (tid == 0) {
+      if (a.rstd) a.rstd[r] = rstd;
+      if (bad) report(a.status, DSPARK_STATUS_BAD_ROW, (int)r);
+    }
+    char* sum = a.sum ? static_cast<char*>(a.sum) + off : nullptr;
+    char* y = static_cast<char*>(a.y) + (E4M3 ? (size_t)r * a.H : off);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * T;
-    if (i >= nvec) continue;
-    if (sum) *reinterpret_cast<uint4*>(sum + (size_t)i * 16) = pack16<DT>(v[j]);
-    float o[N], w[N];
-    unpack16<DT>(wr[j], w);
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * T;
+      if (i >= nvec) continue;
+      if (sum) *reinterpret_cast<uint4*>(sum + (size_t)i * 16) = pack16<DT>(v[j]);
+      float o[N], w[N];
+      unpack16<DT>(wr[j], w);
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = E4M3 ? v[j][e] * w[e] * rstd * inv : v[j][e] * rstd * w[e];
-    if (E4M3)
-      store_e4m3<N>(y + (size_t)i * N, o);
-    else
-      *reinterpret_cast<uint4*>(y + (size_t)i * 16) = pack16<DT>(o);
+      for (int e = 0; e < N; ++e) o[e] = E4M3 ? v[j][e] * w[e] * rstd * inv : v[j][e] * rstd * w[e];
+      if (E4M3)
+        store_e4m3<N>(y + (size_t)i * N, o);
+      else
+        *reinterpret_cast<uint4*>(y + (size_t)i * 16) = pack16<DT>(o);
+    }
   }
 }
 
 // dx = dsum + rstd (w dy - s rstd^2 mean(w dy s)), dweight = sum over rows of
-// dy s rstd. A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ... and keeps
-// its columns' dweight in registers; the CTAs' partial rows are summed in order
-// by a second kernel, so the result does not depend on timing.
+// dy s rstd. A CTA's rows come as above; it keeps its columns' dweight in
+// registers, and the CTAs' partial rows are summed in order by a second kernel, so
+// the result does not depend on timing.
 template <int DT, int NV>
-__global__ void __launch_bounds__(512) norm_grad_kernel(NormGradArgs a) {
-  __shared__ float red[64];
+__global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGradArgs a, int stages) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[kMaxStages];
+  __shared__ float red[2][64];
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
   const int tid = threadIdx.x, T = blockDim.x, nvec = a.H / N;
+  const RowFeed<3> feed = {ring, full,
+                           {static_cast<const char*>(a.s), static_cast<const char*>(a.dy), static_cast<const char*>(a.dsum)},
+                           stages, a.H * es, a.M};
+  feed.start();
+  constexpr bool kKeep = NV * N <= 16;  // weights in registers (else read again, out of L2)
   float dw[NV][N];
+  uint4 wr[kKeep ? NV : 1];
+  auto weights = [&](int j, float* w) {
+    unpack16<DT>(kKeep ? wr[kKeep ? j : 0] : load_raw(static_cast<const char*>(a.weight) + (size_t)(tid + j * T) * 16), w);
+  };
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    if (kKeep && tid + j * T < nvec) wr[kKeep ? j : 0] = load_raw(static_cast<const char*>(a.weight) + (size_t)(tid + j * T) * 16);
 #pragma unroll
     for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
-  for (long long r = blockIdx.x; r < a.M; r += gridDim.x) {
+  }
+  int it = 0;
+  for (long long r = blockIdx.x; r < a.M; r += gridDim.x, ++it) {
     const size_t off = (size_t)r * a.H * es;
-    const float rstd = a.rstd[r];
-    float s[NV][N], g[NV][N];
+    const float rstd = __ldg(a.rstd + r);
+    const bool arrived = feed.wait(it);
+    uint4 sr[NV], gr[NV], dr[NV];
     float dot = 0.f, unused = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * T;
       if (i >= nvec) continue;
-      float w[N];
-      Vec16<DT>::load(static_cast<const char*>(a.s) + off + (size_t)i * 16, s[j]);
-      Vec16<DT>::load(static_cast<const char*>(a.dy) + off + (size_t)i * 16, g[j]);
-      Vec16<DT>::load(static_cast<const char*>(a.weight) + (size_t)i * 16, w);
+      sr[j] = load_raw(feed.row(it, 0) + i * 16);
+      gr[j] = load_raw(feed.row(it, 1) + i * 16);
+      dr[j] = a.dsum ? load_raw(feed.row(it, 2) + i * 16) : make_uint4(0, 0, 0, 0);
+      float s[N], g[N], w[N];
+      unpack16<DT>(sr[j], s);
+      unpack16<DT>(gr[j], g);
+      weights(j, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        dw[j][e] = fmaf(g[j][e] * s[j][e], rstd, dw[j][e]);
-        g[j][e] *= w[e];
-        dot = fmaf(g[j][e], s[j][e], dot);
+        const float gs = g[e] * s[e];
+        dw[j][e] = fmaf(gs, rstd, dw[j][e]);
+        dot = fmaf(gs, w[e], dot);
       }
     }
-    block_sum_max(dot, unused, red);
+    if (block_sum_max(dot, unused, red[it & 1], !arrived)) {  // a wait gave up
+      feed.drain(it);
+      if (tid == 0) report_wait(a.status, kWhereNormRow, (int)r);
+      return;
+    }
+    feed.refill(it);
     const float c = rstd * rstd * (dot / (float)a.H);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * T;
       if (i >= nvec) continue;
-      float d[N];
-      if (a.dsum) {
-        Vec16<DT>::load(static_cast<const char*>(a.dsum) + off + (size_t)i * 16, d);
-      } else {
+      float s[N], g[N], w[N], d[N];
+      unpack16<DT>(sr[j], s);
+      unpack16<DT>(gr[j], g);
+      weights(j, w);
+      unpack16<DT>(dr[j], d);
 #pragma unroll
-        for (int e = 0; e < N; ++e) d[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < N; ++e) d[e] = fmaf(rstd, fmaf(-s[j][e], c, g[j][e]), d[e]);
+      for (int e = 0; e < N; ++e) d[e] = fmaf(rstd, fmaf(-s[e], c, g[e] * w[e]), d[e]);
       *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + off + (size_t)i * 16) = pack16<DT>(d);
     }
-    __syncthreads();  // red is written again by the next row
   }
   if (a.dweight) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * T;
-      if (i < nvec)
+      if (i < nvec) {
+        float4* p = reinterpret_cast<float4*>(a.partial + (size_t)blockIdx.x * a.H + (size_t)i * N);
 #pragma unroll
-        for (int e = 0; e < N; ++e) a.partial[(size_t)blockIdx.x * a.H + (size_t)i * N + e] = dw[j][e];
+        for (int e = 0; e < N; e += 4) p[e / 4] = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+      }
     }
   }
 }
 
-// out[h] = sum over the G partial rows, 32 columns a CTA, 8 rows at a time
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, int G, int H, float* out) {
-  __shared__ float part[8][33];
+// out[h] = sum over the G partial rows: 32 columns a CTA, a warp every 32nd row,
+// four of them in flight (a warp every eighth row one at a time took 7 us for 296
+// rows of 4096, more than twice as long).
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int G, int H, float* out) {
+  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   float acc = 0.f;
-  if (h < H)
-    for (int g = row; g < G; g += 8) acc += partial[(size_t)g * H + h];
+  if (h < H) {
+    for (int g = row; g < G; g += 128) {
+      float d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = g + 32 * j < G ? partial[(size_t)(g + 32 * j) * H + h] : 0.f;
+      acc += (d[0] + d[1]) + (d[2] + d[3]);
+    }
+  }
   part[row][lane] = acc;
   __syncthreads();
-  if (row == 0 && h < H) {
-    float t = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) t += part[q][lane];
-    out[h] = t;
-  }
+  const float t = warp_sum(part[lane][row]);
+  if (lane == 0 && blockIdx.x * 32 + row < H) out[blockIdx.x * 32 + row] = t;
 }
 
-// Vectors per thread: the smallest of 1, 2, 4, 8 that a block of `most` threads
-// covers a row with.
-inline int vecs_per_thread(int nvec, int most) {
-  int nv = 1;
-  while (nv < 8 && nvec > nv * most) nv *= 2;
-  return nv;
+// How a call's rows are cut: threads of a block and vectors per thread (the fewest
+// of 1, 2, 4, 8 that 512 threads cover a row with), blocks per SM, and the ring's
+// depth (up to 4 rows within the SM's shared memory).
+struct Cut {
+  int nv, threads, blocks, stages, smem;
+};
+inline Cut make_cut(int M, int H, int dtype, int arrays, int most_blocks) {
+  const int es = dtype == DSPARK_F32 ? 4 : 2, nvec = H * es / 16, row = arrays * H * es;
+  Cut c;
+  c.nv = 1;
+  while (c.nv < 8 && nvec > c.nv * 512) c.nv *= 2;
+  c.threads = ((nvec + c.nv - 1) / c.nv + 31) / 32 * 32;
+  constexpr int kRing = 216 * 1024;
+  int per_sm = c.nv > most_blocks ? 1 : (c.threads > 256 ? 2 : 4);
+  while (per_sm > 1 && kRing / per_sm < 2 * row) per_sm /= 2;
+  c.stages = max(1, min(kMaxStages, kRing / per_sm / row));
+  c.smem = c.stages * row;
+  c.blocks = min(M, 148 * per_sm);
+  return c;
 }
-inline int threads_for(int nvec, int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; }
+
+template <typename Kern, typename Args>
+cudaError_t launch(Kern kern, const Args& a, const Cut& c, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
+  if (e != cudaSuccess) return e;
+  kern<<<c.blocks, c.threads, c.smem, s>>>(a, c.stages);
+  return cudaGetLastError();
+}
 
 template <int DT, bool E4M3>
 cudaError_t norm_pick(const NormArgs& a, cudaStream_t s) {
-  const int nvec = a.H / Vec16<DT>::N;
-  const int nv = vecs_per_thread(nvec, 256);
-  const int t = threads_for(nvec, nv);
-  const unsigned g = (unsigned)a.M;
-  switch (nv) {
-    case 1: norm_kernel<DT, E4M3, 1><<<g, t, 0, s>>>(a); break;
-    case 2: norm_kernel<DT, E4M3, 2><<<g, t, 0, s>>>(a); break;
-    case 4: norm_kernel<DT, E4M3, 4><<<g, t, 0, s>>>(a); break;
-    default: norm_kernel<DT, E4M3, 8><<<g, t, 0, s>>>(a); break;
+  const Cut c = make_cut(a.M, a.H, DT, 2, 2);
+  switch (c.nv) {
+    case 1: return launch(norm_kernel<DT, E4M3, 1>, a, c, s);
+    case 2: return launch(norm_kernel<DT, E4M3, 2>, a, c, s);
+    case 4: return launch(norm_kernel<DT, E4M3, 4>, a, c, s);
+    default:  // rows of 4-byte entries only: 16384 of 2 bytes are 4 vectors a thread
+      if constexpr (DT == DSPARK_F32) return launch(norm_kernel<DT, E4M3, 8>, a, c, s);
+      return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 template <int DT>
 cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
-  const int nvec = a.H / Vec16<DT>::N;
-  const int nv = vecs_per_thread(nvec, 512);
-  const int t = threads_for(nvec, nv);
-  const unsigned g = (unsigned)min(a.M, kNormGradBlocks);
-  switch (nv) {
-    case 1: norm_grad_kernel<DT, 1><<<g, t, 0, s>>>(a); break;
-    case 2: norm_grad_kernel<DT, 2><<<g, t, 0, s>>>(a); break;
-    case 4: norm_grad_kernel<DT, 4><<<g, t, 0, s>>>(a); break;
-    default:  // rows of 4-byte entries only: 16384 of 2 bytes are 4 vectors a thread
-      if constexpr (DT == DSPARK_F32) norm_grad_kernel<DT, 8><<<g, t, 0, s>>>(a);
-      break;
+  Cut c = make_cut(a.M, a.H, DT, 3, 1);
+  c.blocks = min(c.blocks, kNormGradBlocks);
+  cudaError_t e;
+  switch (c.nv) {
+    case 1: e = launch(norm_grad_kernel<DT, 1>, a, c, s); break;
+    case 2: e = launch(norm_grad_kernel<DT, 2>, a, c, s); break;
+    case 4: e = launch(norm_grad_kernel<DT, 4>, a, c, s); break;
+    default:
+      if constexpr (DT == DSPARK_F32)
+        e = launch(norm_grad_kernel<DT, 8>, a, c, s);
+      else
+        e = cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.dweight) e = column_sums_launch(a.partial, (int)g, a.H, a.dweight, s);
+  if (e == cudaSuccess && a.dweight) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
   return e;
 }
 
 }  // namespace
 
 cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s) {
-  column_sums_kernel<<<(H + 31) / 32, 256, 0, s>>>(partial, G, H, out);
+  column_sums_kernel<<<(H + 31) / 32, 1024, 0, s>>>(partial, G, H, out);
   return cudaGetLastError();
 }
 

@@ -29,9 +29,10 @@ struct NormGradArgs {
   void* dx;             // [M, H]; may be dy or dsum
   float* dweight;       // [H] or null
   float* partial;       // [kNormGradBlocks, H] (workspace)
+  Status* status;
 };
 
-// CTAs of the backward pass, one partial row of dweight each (two for each of 148 SMs)
+// Most CTAs of the backward pass, one partial row of dweight each (two for each of 148 SMs)
 constexpr int kNormGradBlocks = 296;
 
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s);
