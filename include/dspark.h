@@ -110,7 +110,9 @@ enum { DSPARK_CUT_COST = 0, DSPARK_CUT_THRESHOLD = 1, DSPARK_CUT_NONE = 2 };
  * unsupported arguments. The last three operations, whose sizes carry other
  * names, take: LOGPROBS B, K = rows per request (J), V, dtype; NORM B = rows (M),
  * V = width (H); LINEAR B = rows (M), V = outputs (N), r = inputs (K), dtype =
- * the operands' type (BF16 or E4M3). What an operation does not name is ignored.
+ * the operands' type (BF16 or E4M3), and K = 0 for dspark_linear, 1 for
+ * dspark_linear_grad, 2 for dspark_linear_grad with DSPARK_ACT_NONE (which needs no
+ * [M, N] scratch). What an operation does not name is ignored.
  * One workspace of the largest size may serve all the
  * operations of a round: the draft's chunk partials and verification's target
  * statistics occupy different regions of it, so dspark_verify_target_stats may
@@ -408,8 +410,8 @@ int dspark_sts_fit(const float* conf_logit, const uint8_t* survived, int N, int 
  * tok[b,j] = -1 marks padding (dspark_verify's out behind the emitted tokens
  * can be passed as it is): nothing of the row is read, and logp = entropy = lse
  * = 0, top_idx = -1, top_logp = -inf. Rows in error (a token outside [-1, V),
- * NaN, +inf or nothing but -inf among the logits, a negative or NaN
- * temperature) get the same values and set their status bit.
+ * NaN, +inf or nothing but -inf among the logits, a temperature that is negative,
+ * NaN or above 1e30) get the same values and set their status bit.
  *
  *   logits [B, J, V] dtype, tok [B, J] i32, temp [B] f32 or NULL (1)
  *   logp [B, J] f32 out; entropy, lse [B, J] f32 out or NULL
@@ -496,7 +498,8 @@ int dspark_residual_norm_grad(const void* s, const void* weight, const float* rs
  * Limits: 1 <= M, N < 2^24, 1 <= K < 2^20, K a multiple of 16 bytes (8 bf16, 16
  * e4m3 entries); x and w 16-byte aligned, y, pre and residual aligned to their
  * type. Small outputs split K over SMs; the parts are added in a fixed order.
- * Workspace: dspark_workspace_bytes(DSPARK_OP_LINEAR, M, 0, N, K, in_type).
+ * Workspace: dspark_workspace_bytes(DSPARK_OP_LINEAR, M, 0, N, K, in_type) (the
+ * status block alone). One launch.
  */
 int dspark_linear(const void* x, const void* w, const float* x_scale, const float* w_scale,
                   const float* bias, const void* residual, int M, int N, int K, int in_type,
@@ -513,7 +516,8 @@ int dspark_linear(const void* x, const void* w, const float* x_scale, const floa
  *   dx [M, K] bf16, dw [N, K] bf16, dbias [N] f32 out, each NULL to leave it out
  * Limits: those of dspark_linear, and N % 8 == 0; every tensor 16-byte aligned.
  * Outputs must not overlap the inputs.
- * Workspace as for dspark_linear with DSPARK_BF16.
+ * Workspace: dspark_workspace_bytes(DSPARK_OP_LINEAR, M, act ? 1 : 2, N, K,
+ * DSPARK_BF16). Up to four launches: dpre, its column sums, dx, dw.
  */
 int dspark_linear_grad(const void* x, const void* w, const void* dy, const void* pre, int M, int N,
                        int K, int act, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,

@@ -90,7 +90,9 @@ size_t dspark_workspace_bytes(int op, int B, int K, int V, int r, int dtype) {
       return kStatusBytes + (size_t)kNormGradBlocks * V * sizeof(float);
     case DSPARK_OP_LINEAR:
       if (!linear_shape_ok(B, V, r, dtype)) return 0;
-      return kStatusBytes + linear_scratch_bytes(B, V, dtype);
+      if (K < 0 || K > 2) return 0;
+      if (K == 0 || dtype != DSPARK_BF16) return kStatusBytes;  // no backward call in 8 bits
+      return kStatusBytes + linear_scratch_bytes(B, V, K == 1 ? DSPARK_ACT_RELU : DSPARK_ACT_NONE);
     default:
       return 0;
   }

@@ -173,7 +173,7 @@ int dspark_linear_grad(const void* x, const void* w, const void* dy, const void*
   if (!linear_shape_ok(M, N, K, DSPARK_BF16) || N % 8 != 0) return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w) || !aligned16(dy) || !aligned16(pre) || !aligned16(dx) || !aligned16(dw))
     return DSPARK_ERR_INVALID_ARG;
-  if (int e = ws_check(DSPARK_OP_LINEAR, M, 0, N, K, DSPARK_BF16, ws, ws_bytes, nullptr)) return e;
+  if (int e = ws_check(DSPARK_OP_LINEAR, M, act == DSPARK_ACT_NONE ? 2 : 1, N, K, DSPARK_BF16, ws, ws_bytes, nullptr)) return e;
   LinearGradArgs a;
   a.x = x;
   a.w = w;

@@ -668,9 +668,9 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
 
 }  // namespace
 
-size_t linear_scratch_bytes(int M, int N, int in_type) {
-  if (in_type != DSPARK_BF16) return 0;
-  return round_up((size_t)M * N * 2, 256) + round_up((size_t)dpre_runs(M, N) * N * sizeof(float), 256);
+size_t linear_scratch_bytes(int M, int N, int act) {
+  const size_t dpre = act == DSPARK_ACT_NONE ? 0 : round_up((size_t)M * N * 2, 256);
+  return dpre + round_up((size_t)dpre_runs(M, N) * N * sizeof(float), 256);
 }
 
 cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s) {
@@ -703,7 +703,7 @@ cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s) {
 cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   const Plan px = plan_dx(a.M, a.N, a.K), pw = plan_dw(a.M, a.N, a.K);
   char* dpre_buf = a.scratch;
-  float* partial = reinterpret_cast<float*>(dpre_buf + round_up((size_t)a.M * a.N * 2, 256));
+  float* partial = reinterpret_cast<float*>(dpre_buf + (a.act == DSPARK_ACT_NONE ? 0 : round_up((size_t)a.M * a.N * 2, 256)));
   const void* dpre = a.act == DSPARK_ACT_NONE ? a.dy : dpre_buf;
   cudaError_t e;
   if (a.act != DSPARK_ACT_NONE || a.dbias) {

@@ -33,9 +33,9 @@ struct LinearGradArgs {
   Status* status;
 };
 
-// Workspace of the backward call past the status block (dpre and partial column
-// sums; with bf16 operands only).
-size_t linear_scratch_bytes(int M, int N, int in_type);
+// Workspace of the backward call past the status block: dpre (with an activation)
+// and partial column sums.
+size_t linear_scratch_bytes(int M, int N, int act);
 cudaError_t linear_launch(const LinearArgs& a, cudaStream_t s);
 cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s);
 

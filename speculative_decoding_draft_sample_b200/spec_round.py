@@ -14,6 +14,7 @@ import torch
 
 from . import binding as bn
 from . import replicas
+from .heads import LogitHead, TokenScores
 
 # Most SMs a round's draft leaves to the side stream, and how much longer the
 # draft may get for it (the ratio of the most vocabulary tiles per CTA to the
@@ -106,6 +107,10 @@ class SpecRound:
         self.q_tok = torch.empty((B, K), **f32)
         self.q_norm = torch.empty((B, K, 2), **f32)  # the draws' normalisers, for verify
         self.h = None  # the recurrent head's states [B, K, r], when a round uses it
+        # logits made from hidden states, when a round is given heads
+        self.target = self.base = None
+        self.verified = None  # the target logits of the last run
+        self.scores: Optional[TokenScores] = None
         self.cut = torch.empty((B,), **i32)
         self.survival = torch.empty((B, K), **f32)
         self.accepted = torch.empty((B,), **i32)
@@ -122,8 +127,16 @@ class SpecRound:
 
     def run(self, inp: Dict[str, torch.Tensor], seed: int, round_id: int,
             mode: int = bn.CUT_COST, threshold: float = 0.0, stream=None,
-            side_stream=None, global_schedule: Optional[GlobalSchedule] = None) -> None:
+            side_stream=None, global_schedule: Optional[GlobalSchedule] = None,
+            target_head: Optional[LogitHead] = None,
+            draft_head: Optional[LogitHead] = None) -> None:
         """Issues the round on ``stream`` (no host synchronisation).
+
+        With ``target_head`` the target logits come from the target model's hidden
+        states ``inp["target_hidden"]`` [B, K+1, H] (and ``inp["target_delta"]``, its last
+        layer's output still to be added, where given) instead of ``inp["target"]``; with
+        ``draft_head`` the base logits from ``inp["base_hidden"]`` [B, K, H] likewise. Both
+        heads run first, on ``stream``.
 
         The prefix schedule needs only the confidence logits, and the target
         rows' statistics only the target logits and the cut, so with a
@@ -135,6 +148,13 @@ class SpecRound:
         meet only in its status block, which every call updates atomically.
         """
         main = stream if stream is not None else torch.cuda.current_stream(self.x.device)
+        if target_head is not None:
+            self.target = self._logits(self.target, self.K + 1, target_head, inp, "target", main)
+            inp = dict(inp, target=self.target)
+        if draft_head is not None:
+            self.base = self._logits(self.base, self.K, draft_head, inp, "base", main)
+            inp = dict(inp, base=self.base)
+        self.verified = inp["target"]
 
         def schedule_and_stats(s):
             if global_schedule is not None:  # one cut over every rank's requests
@@ -179,19 +199,46 @@ class SpecRound:
                              seed, round_id, self.accepted, self.out, self.n_emit, self.ws, main,
                              q_norm=self.q_norm)
 
+    def _logits(self, out, J: int, head: LogitHead, inp, name: str, stream):
+        if head.V != self.V:
+            raise bn.DSparkError(f"the head's vocabulary is {head.V}, the round's {self.V}")
+        hidden = inp[name + "_hidden"]
+        if tuple(hidden.shape) != (self.B, J, head.H):
+            raise bn.DSparkError(f"{name}_hidden must have shape {(self.B, J, head.H)}, got {tuple(hidden.shape)}")
+        if out is None:
+            out = torch.empty((self.B, J, self.V), dtype=self.dtype, device=self.x.device)
+        head.run(hidden, out, delta=inp.get(name + "_delta"), stream=stream)
+        return out
+
+    def score(self, temp: Optional[torch.Tensor], n_top: int = 0, stream=None) -> TokenScores:
+        """Scores the tokens the last ``run`` emitted (``out``) against the target logits it
+        verified with, at temperatures ``temp`` [B] (the round's, or None for 1): their log
+        probabilities, entropies and n_top alternatives, zeros and -1 behind the emitted
+        tokens. Row j of a request holds its j-th emitted token. The scores stay in buffers
+        of this round that the next call overwrites."""
+        if self.verified is None:
+            raise bn.DSparkError("score() needs a run() before it")
+        if self.scores is None or (0 if self.scores.top_idx is None else self.scores.top_idx.shape[2]) != n_top:
+            self.scores = TokenScores(self.B, self.K + 1, self.V, n_top, self.dtype, self.x.device)
+        self.scores.run(self.verified, self.out, temp, stream=stream)
+        return self.scores
+
     def status(self, stream=None):
         return bn.read_status(self.ws, stream)
 
 
 DEVICE_KEYS = ("base", "target", "U", "W", "bias_scale", "last_tok", "temp", "conf_logit",
                "pos_temp", "step_cost")
-OPTIONAL_KEYS = ("R",)  # the recurrent head's state matrix
+HIDDEN_KEYS = ("target_hidden", "target_delta", "base_hidden", "base_delta")  # in place of logits, with heads
+OPTIONAL_KEYS = ("R",) + HIDDEN_KEYS  # R: the recurrent head's state matrix
 
 
 def to_device(inp: Dict[str, object], device: str = "cuda", pin: bool = False) -> Dict[str, object]:
     """Device (or pinned host) copies of a workload's tensors (numpy arrays become tensors)."""
     out: Dict[str, object] = {}
     for k in DEVICE_KEYS:
+        if inp.get(k) is None and inp.get(k + "_hidden") is not None:
+            continue  # made by a head
         v = inp[k]
         t = v if isinstance(v, torch.Tensor) else torch.from_numpy(v)
         if k == "last_tok":
@@ -212,11 +259,18 @@ def to_device(inp: Dict[str, object], device: str = "cuda", pin: bool = False) -
 def run_host(rnd: SpecRound, host: Dict[str, object], dev: Dict[str, object], seed: int,
              round_id: int, out_host: torch.Tensor, n_emit_host: torch.Tensor,
              mode: int = bn.CUT_COST, stream=None, side_stream=None,
-             threshold: float = 0.0, global_schedule: Optional[GlobalSchedule] = None) -> None:
-    """End to end from pinned host buffers: H2D copies, the round, D2H of the tokens."""
+             threshold: float = 0.0, global_schedule: Optional[GlobalSchedule] = None,
+             target_head: Optional[LogitHead] = None, draft_head: Optional[LogitHead] = None) -> None:
+    """End to end from pinned host buffers: H2D copies, the round (from logits, or from
+    hidden states and heads), D2H of the tokens."""
     for k in DEVICE_KEYS:
+        if host.get(k) is None and host.get(k + "_hidden") is not None:
+            continue  # made by a head
         dev[k].copy_(host[k], non_blocking=True)
+    for k in HIDDEN_KEYS:
+        if host.get(k) is not None:
+            dev[k].copy_(host[k], non_blocking=True)
     rnd.run(dev, seed, round_id, mode, threshold, stream=stream, side_stream=side_stream,
-            global_schedule=global_schedule)
+            global_schedule=global_schedule, target_head=target_head, draft_head=draft_head)
     out_host.copy_(rnd.out, non_blocking=True)
     n_emit_host.copy_(rnd.n_emit, non_blocking=True)

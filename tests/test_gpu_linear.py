@@ -30,8 +30,8 @@ def operand(rows, K, e4m3, g, std=1.0):
     return (v / scale[:, None]).to(E4M3), scale
 
 
-def workspace(M, N, K, code=bn.BF16):
-    n = bn.workspace_bytes(bn.OP_LINEAR, M, 0, N, K, code)
+def workspace(M, N, K, code=bn.BF16, mode=0):
+    n = bn.workspace_bytes(bn.OP_LINEAR, M, mode, N, K, code)
     assert n > 0
     return torch.full((n,), 255, dtype=torch.uint8, device="cuda").index_fill_(0, torch.arange(256, device="cuda"), 0)
 
@@ -152,7 +152,7 @@ def test_gradient_matches(cuda_ok, M, N, K, act):
     pre[0, 0] = 0
     dx, dw = torch.full_like(x, 7), torch.full_like(w, 7)
     db = torch.full((N,), 7.0, device="cuda")
-    ws = workspace(M, N, K)
+    ws = workspace(M, N, K, mode=1 if act != "none" else 2)
     bn.linear_grad(x, w, dy, ws, dx=dx, dw=dw, dbias=db, pre=pre if act != "none" else None, act=act)
     torch.cuda.synchronize()
     assert bn.read_status(ws) == (0, -1)
@@ -178,7 +178,7 @@ def test_gradient_parts_alone(cuda_ok):
     w, _ = operand(N, K, False, g)
     dy = torch.randn(M, N, generator=g, device="cuda").to(BF16)
     every = dict(dx=torch.empty_like(x), dw=torch.empty_like(w), dbias=torch.empty(N, device="cuda"))
-    ws = workspace(M, N, K)
+    ws = workspace(M, N, K, mode=1)
     bn.linear_grad(x, w, dy, ws, pre=dy, act="gelu", **every)
     for k, v in every.items():
         one = torch.full_like(v, 7)
@@ -203,7 +203,7 @@ def test_gradient_against_differences(cuda_ok):
     out, pre = torch.empty(M, N, device="cuda", dtype=BF16), torch.empty(M, N, device="cuda", dtype=BF16)
     bn.linear(x, w, out, workspace(M, N, K), pre=pre, act="silu")
     dx = torch.empty_like(x)
-    bn.linear_grad(x, w, dy, workspace(M, N, K), dx=dx, pre=pre, act="silu")
+    bn.linear_grad(x, w, dy, workspace(M, N, K, mode=1), dx=dx, pre=pre, act="silu")
     S = (dy.double().abs() @ w.double().abs())[0]
     # silu'' and silu''' stay below 0.6; pre moved by 2^-9 of its size (at most 8); two roundings of 2^-8
     tol = S * (h * h / 6 * 0.6 + 0.6 * 8 * 2.0 ** -9 + 2 * 2.0 ** -8) + 1e-4
@@ -211,7 +211,7 @@ def test_gradient_against_differences(cuda_ok):
 
 
 def test_captured_shared_workspace_and_side_stream(cuda_ok):
-    M, N, K = 12, 300, 4096                  # split: counters and partial sums in the workspace
+    M, N, K = 12, 300, 4096                  # the contraction is split over a cluster
     g = torch.Generator(device="cuda").manual_seed(4)
     x, _ = operand(M, K, False, g)
     w, _ = operand(N, K, False, g)

@@ -1,0 +1,214 @@
+"""The operators together, as a round uses them: hidden states -> logits -> round -> scores,
+and the gradient back to the hidden states.
+
+Tolerances of the head: y carries half a step of its type (bf16 2^-9 of the value; e4m3
+2^-4, 2^-10 of its scale below the normal range), each of the H products brings that
+share, the accumulator 2^-23 (H / 16 + 156) of the sum of magnitudes, the logit half a
+step of its own type.
+"""
+import pytest
+import torch
+
+from parity import SEED
+from speculative_decoding_draft_sample_b200 import binding as bn
+from speculative_decoding_draft_sample_b200 import workloads as wl
+from speculative_decoding_draft_sample_b200.heads import LogitHead, TokenScores, quantize_rows
+from speculative_decoding_draft_sample_b200.spec_round import SpecRound, run_host, to_device
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+H = 512
+
+
+def parts(V, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    norm_w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(BF16)
+    w = (torch.randn(V, H, generator=g, device="cuda") * 2 * H ** -0.5).to(BF16)
+    return norm_w, w, g
+
+
+def hidden(g, *shape):
+    return (torch.randn(*shape, H, generator=g, device="cuda") * 3).to(BF16)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,J", [(1, 1), (3, 5), (40, 6)])
+def test_head_matches_the_definition(cuda_ok, B, J, e4m3, out):
+    V = 1000
+    norm_w, w, g = parts(V)
+    x, delta = hidden(g, B, J), hidden(g, B, J)
+    bias = torch.randn(V, generator=g, device="cuda")
+    q, scale = quantize_rows(w) if e4m3 else (w, None)
+    head = LogitHead(norm_w, q, B * J + 7, w_scale=scale, bias=bias)
+    logits = torch.empty(B, J, V, device="cuda", dtype=out)
+    head.run(x, logits, delta=delta)
+    assert head.status() == (0, -1)
+    v = (x.double() + delta.double()).view(B * J, H)
+    y = v / torch.sqrt(v.square().mean(1, keepdim=True) + 1e-6) * norm_w.double()
+    wd = q.double() * (scale.double()[:, None] if e4m3 else 1)
+    want = (y @ wd.t() + bias.double()).view(B, J, V)
+    S = (y.abs() @ wd.abs().t()).view(B, J, V)
+    step = 2.0 ** -4 if e4m3 else 2.0 ** -9
+    low = 2.0 ** -10 * (y.abs().amax(1) / 448).view(B, J, 1) * wd.abs().sum(1) if e4m3 else 0
+    tol = (step + 2.0 ** -17 + 2.0 ** -23 * (H / 16 + 156)) * S + low
+    tol = tol + (torch.finfo(out).eps / 2 + 2.0 ** -22) * (want.abs() + tol + bias.double().abs())
+    assert bool(((logits.double() - want).abs() <= tol).all())
+    assert torch.equal(head.sum[:B * J], (x.float() + delta.float()).to(BF16).view(-1, H))
+
+
+def round_inputs(e4m3=False, greedy=0.0):
+    w = wl.scaled(wl.DSPARK5, name="heads", B=24, K=4, V=4096, greedy_frac=greedy)
+    inp = wl.generate(w)
+    norm_w, weight, g = parts(w.V, seed=3)
+    q, scale = quantize_rows(weight) if e4m3 else (weight, None)
+    th, dh = LogitHead(norm_w, q, w.B * (w.K + 1), w_scale=scale), LogitHead(norm_w, q, w.B * w.K, w_scale=scale)
+    host = {k: v for k, v in inp.items() if k not in ("target", "base")}
+    t = hidden(g, w.B, w.K + 1)
+    host["target_hidden"] = t.cpu()
+    host["target_delta"] = hidden(g, w.B, w.K + 1).cpu()
+    host["base_hidden"] = (t[:, :w.K].float() + torch.randn(w.B, w.K, H, generator=g, device="cuda")).to(BF16).cpu()
+    return w, host, th, dh
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_round_from_hidden_states(cuda_ok, e4m3):
+    w, host, th, dh = round_inputs(e4m3, greedy=0.25)
+    dev = to_device(host)
+    rnd = SpecRound(w.B, w.K, w.V, w.r)
+    rnd.run(dev, SEED, 2, target_head=th, draft_head=dh)
+    # the same round from logits that the heads made on their own
+    target = torch.empty(w.B, w.K + 1, w.V, device="cuda", dtype=BF16)
+    base = torch.empty(w.B, w.K, w.V, device="cuda", dtype=BF16)
+    th.run(dev["target_hidden"], target, delta=dev["target_delta"])
+    dh.run(dev["base_hidden"], base)
+    plain = SpecRound(w.B, w.K, w.V, w.r)
+    plain.run(dict(dev, target=target, base=base), SEED, 2)
+    torch.cuda.synchronize()
+    assert rnd.status() == (0, -1) and plain.status() == (0, -1)
+    for name in ("x", "d", "cut", "accepted", "out", "n_emit"):
+        assert torch.equal(getattr(rnd, name), getattr(plain, name)), name
+    assert int(rnd.accepted.sum()) > 0
+    # from pinned host memory, the statistics on a side stream
+    pinned = to_device(host, pin=True)
+    live = {k: torch.zeros_like(v, device="cuda") if torch.is_tensor(v) else v for k, v in pinned.items()}
+    out_h, n_h = torch.empty(w.B, w.K + 1, dtype=torch.int32).pin_memory(), torch.empty(w.B, dtype=torch.int32).pin_memory()
+    side = torch.cuda.Stream()
+    run_host(rnd, pinned, live, SEED, 2, out_h, n_h, side_stream=side, target_head=th, draft_head=dh)
+    torch.cuda.synchronize()
+    assert torch.equal(out_h, plain.out.cpu()) and torch.equal(n_h, plain.n_emit.cpu())
+
+
+def test_scores_of_the_emitted_tokens(cuda_ok):
+    w, host, th, dh = round_inputs(greedy=0.25)
+    dev = to_device(host)
+    rnd = SpecRound(w.B, w.K, w.V, w.r)
+    with pytest.raises(bn.DSparkError, match="needs a run"):
+        rnd.score(dev["temp"])
+    rnd.run(dev, SEED, 5, target_head=th, draft_head=dh)
+    s = rnd.score(dev["temp"], n_top=6)
+    torch.cuda.synchronize()
+    assert s.status() == (0, -1)
+    emitted = torch.arange(w.K + 1, device="cuda") < rnd.n_emit[:, None]
+    assert torch.equal(rnd.out >= 0, emitted)
+    temp = torch.where(dev["temp"] > 0, dev["temp"], torch.ones_like(dev["temp"])).double()
+    lp = torch.log_softmax(rnd.verified.double() / temp[:, None, None], -1)
+    want = lp.gather(-1, rnd.out.clamp(min=0).long()[..., None])[..., 0]
+    e = 2.0 ** -24 * (w.V / 256 + 16) + 2.0 ** -22 + 2.0 ** -23 * 30
+    err = (s.logp.double() - want).abs()
+    assert bool((err[emitted] <= e + 2.0 ** -22 * want.abs()[emitted]).all())
+    assert bool((s.logp[~emitted] == 0).all() and (s.top_idx[~emitted] == -1).all())
+    order = torch.sort(rnd.verified.double(), dim=-1, descending=True, stable=True).indices[..., :6].int()
+    assert torch.equal(s.top_idx[emitted], order[emitted])
+    # greedy requests emit the most likely token of every row
+    greedy = (dev["temp"] == 0)[:, None] & emitted
+    assert torch.equal(rnd.out[greedy], s.top_idx[..., 0][greedy])
+
+
+def test_round_with_heads_and_scores_in_a_graph(cuda_ok):
+    w, host, th, dh = round_inputs()
+    dev = to_device(host)
+    rnd = SpecRound(w.B, w.K, w.V, w.r)
+    rnd.run(dev, SEED, 1, target_head=th, draft_head=dh)
+    s = rnd.score(dev["temp"], n_top=3)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (rnd.out, s.logp, s.entropy, s.top_idx)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rnd.run(dev, SEED, 1, target_head=th, draft_head=dh)
+        rnd.score(dev["temp"], n_top=3)
+    for _ in range(2):
+        for t in (rnd.out, s.logp, s.entropy, s.top_idx):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, v in zip((rnd.out, s.logp, s.entropy, s.top_idx), want):
+            assert torch.equal(t, v)
+
+
+def test_gradient_from_scores_to_hidden_states(cuda_ok):
+    """The chain scores -> head against autograd in 64 bits. dlogits is rounded to bf16 (2^-9 of
+    each entry), the normalised y that enters dweight too; dx is rounded to bf16 between the two
+    calls and at the end. Errors are taken relative to the norm of each output, where independent
+    half steps of 2^-9 stay below 2^-9 each: 4 of them, and 2^-12 for everything in fp32."""
+    B, J, V = 6, 4, 2048
+    norm_w, w, g = parts(V, seed=7)
+    x, delta = hidden(g, B, J), hidden(g, B, J)
+    tok = torch.randint(0, V, (B, J), generator=g, device="cuda", dtype=torch.int32)
+    tok[2, 2:] = -1
+    temp = torch.tensor([0.7, 1.0, 1.3, 0.9, 1.0, 2.0], device="cuda")
+    gl, gh = torch.randn(B, J, generator=g, device="cuda"), 0.1 * torch.randn(B, J, generator=g, device="cuda")
+    head, scores = LogitHead(norm_w, w, B * J), TokenScores(B, J, V, dtype=BF16)
+    logits = torch.empty(B, J, V, device="cuda", dtype=BF16)
+    head.run(x, logits, delta=delta)
+    scores.run(logits, tok, temp)
+    dlogits = torch.empty_like(logits)
+    scores.gradient(logits, tok, temp, gl, dlogits, g_entropy=gh)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    db, dn = torch.empty(V, device="cuda"), torch.empty(H, device="cuda")
+    head.gradient(dlogits, dx, dweight=dw, dbias=db, dnorm_weight=dn)
+    assert head.status() == (0, -1) and scores.status() == (0, -1)
+    frozen = torch.empty_like(x)
+    head.gradient(dlogits, frozen)
+    assert torch.equal(frozen, dx)
+
+    xs = head.sum.double().view(B, J, H).requires_grad_()
+    nw, ww = norm_w.double().requires_grad_(), w.double().requires_grad_()
+    bias = torch.zeros(V, device="cuda", dtype=torch.float64, requires_grad=True)
+    y = xs / torch.sqrt(xs.square().mean(-1, keepdim=True) + 1e-6) * nw
+    z = y @ ww.t() + bias
+    z = z + (logits.double() - z).detach()      # the stored logits are what was scored
+    lp = torch.log_softmax(z / temp.double()[:, None, None], -1)
+    keep = tok >= 0
+    loss = ((lp.gather(-1, tok.clamp(min=0).long()[..., None])[..., 0] * gl.double())[keep].sum()
+            - ((lp.exp() * lp).sum(-1) * gh.double())[keep].sum())
+    want = torch.autograd.grad(loss, (xs, ww, bias, nw))
+    for got, ref in zip((dx, dw, db, dn), want):
+        rel = ((got.double() - ref).norm() / ref.norm()).item()
+        assert rel <= 4 * 2.0 ** -9 + 2.0 ** -12, rel
+    assert bool((dx[2, 2:] == 0).all())
+
+
+def test_heads_refuse_what_does_not_fit(cuda_ok):
+    norm_w, w, g = parts(256)
+    q, scale = quantize_rows(w)
+    with pytest.raises(bn.DSparkError, match="w_scale goes"):
+        LogitHead(norm_w, q, 4)
+    with pytest.raises(bn.DSparkError, match="norm_weight must have shape"):
+        LogitHead(norm_w[:8], w, 4)
+    with pytest.raises(bn.DSparkError, match="bfloat16 or float8"):
+        LogitHead(norm_w, w.float(), 4)
+    head = LogitHead(norm_w, w, 4)
+    with pytest.raises(bn.DSparkError, match="do not fit"):
+        head.run(hidden(g, 5), torch.empty(5, 256, device="cuda", dtype=BF16))
+    with pytest.raises(bn.DSparkError, match="do not fit"):
+        head.run(hidden(g, 4), torch.empty(4, 264, device="cuda", dtype=BF16))
+    with pytest.raises(bn.DSparkError, match="contiguous"):
+        head.run(hidden(g, 8)[::2], torch.empty(4, 256, device="cuda", dtype=BF16))
+    with pytest.raises(bn.DSparkError, match="no gradient"):
+        LogitHead(norm_w, q, 4, w_scale=scale).gradient(torch.empty(4, 256, device="cuda", dtype=BF16), hidden(g, 4))
+    with pytest.raises(bn.DSparkError, match="n_top"):
+        TokenScores(2, 2, 64, n_top=33)
+    rnd = SpecRound(4, 2, 512, 64)
+    with pytest.raises(bn.DSparkError, match="vocabulary"):
+        rnd.run({"target_hidden": hidden(g, 4, 3)}, SEED, 0, target_head=head)

@@ -208,4 +208,10 @@ def test_workspace_sizes(lib):
     assert bn.workspace_bytes(bn.OP_NORM, 7, 0, 4100, 0, 0) == 0
     assert bn.workspace_bytes(bn.OP_LINEAR, 7, 0, 100, 4100, bn.BF16) == 0
     assert bn.workspace_bytes(bn.OP_LINEAR, 7, 0, 100, 4096, bn.F32) == 0
-    assert bn.workspace_bytes(bn.OP_LINEAR, 1, 0, 1, 16, bn.E4M3) >= 256
+    assert bn.workspace_bytes(bn.OP_LINEAR, 1, 0, 1, 16, bn.E4M3) == 256
+    assert bn.workspace_bytes(bn.OP_LINEAR, 1536, 0, 129280, 4096, bn.BF16) == 256
+    assert bn.workspace_bytes(bn.OP_LINEAR, 1, 1, 8, 16, bn.E4M3) == 256    # no backward call in 8 bits
+    assert bn.workspace_bytes(bn.OP_LINEAR, 40, 3, 8, 16, bn.BF16) == 0
+    # backward: dpre (with an activation) and column sums of up to ceil(M / 32) runs of rows
+    assert bn.workspace_bytes(bn.OP_LINEAR, 40, 2, 256, 16, bn.BF16) == 256 + 2 * 256 * 4
+    assert bn.workspace_bytes(bn.OP_LINEAR, 40, 1, 256, 16, bn.BF16) == 256 + 40 * 256 * 2 + 2 * 256 * 4
