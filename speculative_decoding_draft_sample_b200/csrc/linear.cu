@@ -69,7 +69,7 @@ enum : unsigned int {  // wait sites recorded when a bounded wait gives up
 struct Gemm {
   int F, T;                 // lanes (contiguous outputs) and columns in all
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
-  int nt;                   // columns per tile, a multiple of 16 (128 when B is column-contiguous)
+  int nt;                   // columns per tile, a multiple of 16 (32 when B is column-contiguous)
   int tiles_f, tiles_t;
   int parts;                // pairs that share a tile (1, 2, 4 or 8)
   const float* col_scale;   // [T] or null
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part = cluster_rank >> 1;  // the pair's part of the contraction
   const int kb0 = (int)((long long)g.kblocks * part / g.parts), kb1 = (int)((long long)g.kblocks * (part + 1) / g.parts);
   const int nh = g.nt / 2;  // columns of B in this CTA
-  const int stage_bytes = kABytes + nh * 128;
+  const int stage_bytes = kABytes + (B_MN ? (nh + 63) / 64 * kBoxBytes : nh * 128);
   const int stages = min(kMaxStages, kRing / stage_bytes);
   Tiles w(g, blockIdx.x / (2 * g.parts), gridDim.x / (2 * g.parts));
 
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(a, &map_a, kx, f0, bar);
           }
           if (B_MN) {
-            for (int q = 0; q < nh / 64; ++q) tma_load_2d(b + q * kBoxBytes, &map_b, t0 + q * 64, kx, bar);
+            for (int q = 0; q < (nh + 63) / 64; ++q) tma_load_2d(b + q * kBoxBytes, &map_b, t0 + q * 64, kx, bar);
           } else {
             tma_load_2d(b, &map_b, kx, t0, bar);
           }
@@ -600,7 +600,7 @@ Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
   double best_cost = 1e300;
   for (int i = 0; i < 10; ++i) {
     const int nt = kWidths[i];
-    if (b_cols && nt % 128 != 0) continue;
+    if (b_cols && nt % 32 != 0) continue;  // a CTA's half starts at a whole 16 bytes of the columns
     const double block = kBlockNs[i], epilogue = 600.0 + 9.5 * nt;
     for (int j = 0; j < 4; ++j) {
       const int parts = 1 << j, at_once = kAtOnce[j];
@@ -709,6 +709,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   if (a.act != DSPARK_ACT_NONE || a.dbias) {
     const int runs = dpre_runs(a.M, a.N);
     const int rows_per = (a.M + runs - 1) / runs;
+    if (runs == 1) partial = a.dbias;  // one run's sums are the result
     auto kern = a.act == DSPARK_ACT_RELU   ? dpre_kernel<DSPARK_ACT_RELU>
                 : a.act == DSPARK_ACT_SILU ? dpre_kernel<DSPARK_ACT_SILU>
                 : a.act == DSPARK_ACT_GELU ? dpre_kernel<DSPARK_ACT_GELU>
@@ -716,7 +717,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
     kern<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, rows_per, dpre_buf, a.dbias ? partial : nullptr);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.dbias && (e = column_sums_launch(partial, runs, a.N, a.dbias, s)) != cudaSuccess) return e;
+    if (a.dbias && runs > 1 && (e = column_sums_launch(partial, runs, a.N, a.dbias, s)) != cudaSuccess) return e;
   }
   CUtensorMap ma, mb;
   Gemm g = {};

@@ -74,6 +74,82 @@ __device__ __forceinline__ bool block_sum_max(float& s, float& m, float* red, bo
   return any;
 }
 
+// sum v^2 and max |v w| of a vector added to ss and mx
+template <int DT, bool E4M3>
+__device__ __forceinline__ void add_row(const float* v, const uint4& wr, float& ss, float& mx) {
+  constexpr int N = Vec16<DT>::N;
+  float w[N];
+  if (E4M3) unpack16<DT>(wr, w);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    ss = fmaf(v[e], v[e], ss);
+    if (E4M3) mx = max_nan(mx, fabsf(v[e] * w[e]));
+  }
+}
+
+// (rstd, 1 / scale) of row r from its sums; one thread writes them out.
+template <bool E4M3>
+__device__ __forceinline__ float2 row_factors(const NormArgs& a, long long r, float ss, float mx, bool one) {
+  // NaN or a sum of squares past fp32 makes the whole row NaN
+  const bool bad = !(ss < INFINITY) || (E4M3 && !(mx < INFINITY));
+  const float rstd = bad ? NAN : 1.f / sqrtf(ss / (float)a.H + a.eps);
+  float inv = 1.f;  // 1 / scale: finite, as the scale is a normal number
+  if (E4M3) {
+    const float scale = bad ? NAN : fmaxf(mx * rstd / kE4m3Max, kMinScale);
+    inv = 1.f / scale;
+    if (one) a.y_scale[r] = scale;
+  }
+  if (one) {
+    if (a.rstd) a.rstd[r] = rstd;
+    if (bad) report(a.status, DSPARK_STATUS_BAD_ROW, (int)r);
+  }
+  return make_float2(rstd, inv);
+}
+
+// Vector i of row r: the sum and y.
+template <int DT, bool E4M3>
+__device__ __forceinline__ void write_row(const NormArgs& a, long long r, int i, const float* v, const uint4& wr, float2 k) {
+  constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
+  const size_t off = (size_t)r * a.H * es + (size_t)i * 16;
+  if (a.sum) *reinterpret_cast<uint4*>(static_cast<char*>(a.sum) + off) = pack16<DT>(v);
+  float o[N], w[N];
+  unpack16<DT>(wr, w);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = E4M3 ? v[e] * w[e] * k.x * k.y : v[e] * k.x * w[e];
+  if (E4M3)
+    store_e4m3<N>(static_cast<char*>(a.y) + (size_t)r * a.H + (size_t)i * N, o);
+  else
+    *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + off) = pack16<DT>(o);
+}
+
+// A vector's share of dweight and of sum w dy s.
+template <int DT>
+__device__ __forceinline__ void add_grad(const uint4& sr, const uint4& gr, const float* w, float rstd, float* dw, float& dot) {
+  constexpr int N = Vec16<DT>::N;
+  float s[N], g[N];
+  unpack16<DT>(sr, s);
+  unpack16<DT>(gr, g);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float gs = g[e] * s[e];
+    dw[e] = fmaf(gs, rstd, dw[e]);
+    dot = fmaf(gs, w[e], dot);
+  }
+}
+
+// dx of a vector; c = rstd^2 mean(w dy s)
+template <int DT>
+__device__ __forceinline__ uint4 grad16(const uint4& sr, const uint4& gr, const uint4& dr, const float* w, float rstd, float c) {
+  constexpr int N = Vec16<DT>::N;
+  float s[N], g[N], d[N];
+  unpack16<DT>(sr, s);
+  unpack16<DT>(gr, g);
+  unpack16<DT>(dr, d);
+#pragma unroll
+  for (int e = 0; e < N; ++e) d[e] = fmaf(rstd, fmaf(-s[e], c, g[e] * w[e]), d[e]);
+  return pack16<DT>(d);
+}
+
 enum : unsigned int { kWhereNormRow = 60 };  // wait site recorded when a bounded wait gives up
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -151,7 +227,6 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) norm_kernel(NormArgs a, 
   int it = 0;
   for (long long r = blockIdx.x; r < a.M; r += gridDim.x, ++it) {
     const bool arrived = feed.wait(it);
-    const size_t off = (size_t)r * a.H * es;
     float v[NV][N];
     float ss = 0.f, mx = 0.f;
 #pragma unroll
@@ -165,13 +240,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) norm_kernel(NormArgs a, 
 #pragma unroll
         for (int e = 0; e < N; ++e) v[j][e] += d[e];
       }
-      float w[N];
-      if (E4M3) unpack16<DT>(wr[j], w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        ss = fmaf(v[j][e], v[j][e], ss);
-        if (E4M3) mx = max_nan(mx, fabsf(v[j][e] * w[e]));
-      }
+      add_row<DT, E4M3>(v[j], wr[j], ss, mx);
     }
     if (block_sum_max(ss, mx, red[it & 1], !arrived)) {  // a wait gave up
       feed.drain(it);
@@ -179,35 +248,10 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) norm_kernel(NormArgs a, 
       return;
     }
     feed.refill(it);
-    // NaN or a sum of squares past fp32 makes the whole row NaN
-    const bool bad = !(ss < INFINITY) || (E4M3 && !(mx < INFINITY));
-    const float rstd = bad ? NAN : 1.f / sqrtf(ss / (float)a.H + a.eps);
-    float inv = 1.f;  // 1 / scale: finite, as the scale is a normal number
-    if (E4M3) {
-      const float scale = bad ? NAN : fmaxf(mx * rstd / kE4m3Max, kMinScale);
-      inv = 1.f / scale;
-      if (tid == 0) a.y_scale[r] = scale;
-    }
-    if (tid == 0) {
-      if (a.rstd) a.rstd[r] = rstd;
-      if (bad) report(a.status, DSPARK_STATUS_BAD_ROW, (int)r);
-    }
-    char* sum = a.sum ? static_cast<char*>(a.sum) + off : nullptr;
-    char* y = static_cast<char*>(a.y) + (E4M3 ? (size_t)r * a.H : off);
+    const float2 k = row_factors<E4M3>(a, r, ss, mx, tid == 0);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * T;
-      if (i >= nvec) continue;
-      if (sum) *reinterpret_cast<uint4*>(sum + (size_t)i * 16) = pack16<DT>(v[j]);
-      float o[N], w[N];
-      unpack16<DT>(wr[j], w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = E4M3 ? v[j][e] * w[e] * rstd * inv : v[j][e] * rstd * w[e];
-      if (E4M3)
-        store_e4m3<N>(y + (size_t)i * N, o);
-      else
-        *reinterpret_cast<uint4*>(y + (size_t)i * 16) = pack16<DT>(o);
-    }
+    for (int j = 0; j < NV; ++j)
+      if (tid + j * T < nvec) write_row<DT, E4M3>(a, r, tid + j * T, v[j], wr[j], k);
   }
 }
 
@@ -228,7 +272,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
   feed.start();
   constexpr bool kKeep = NV * N <= 16;  // weights in registers (else read again, out of L2)
   float dw[NV][N];
-  uint4 wr[kKeep ? NV : 1];
+  uint4 wr[kKeep ? NV : 1] = {};
   auto weights = [&](int j, float* w) {
     unpack16<DT>(kKeep ? wr[kKeep ? j : 0] : load_raw(static_cast<const char*>(a.weight) + (size_t)(tid + j * T) * 16), w);
   };
@@ -252,16 +296,9 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
       sr[j] = load_raw(feed.row(it, 0) + i * 16);
       gr[j] = load_raw(feed.row(it, 1) + i * 16);
       dr[j] = a.dsum ? load_raw(feed.row(it, 2) + i * 16) : make_uint4(0, 0, 0, 0);
-      float s[N], g[N], w[N];
-      unpack16<DT>(sr[j], s);
-      unpack16<DT>(gr[j], g);
+      float w[N];
       weights(j, w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float gs = g[e] * s[e];
-        dw[j][e] = fmaf(gs, rstd, dw[j][e]);
-        dot = fmaf(gs, w[e], dot);
-      }
+      add_grad<DT>(sr[j], gr[j], w, rstd, dw[j], dot);
     }
     if (block_sum_max(dot, unused, red[it & 1], !arrived)) {  // a wait gave up
       feed.drain(it);
@@ -274,14 +311,9 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * T;
       if (i >= nvec) continue;
-      float s[N], g[N], w[N], d[N];
-      unpack16<DT>(sr[j], s);
-      unpack16<DT>(gr[j], g);
+      float w[N];
       weights(j, w);
-      unpack16<DT>(dr[j], d);
-#pragma unroll
-      for (int e = 0; e < N; ++e) d[e] = fmaf(rstd, fmaf(-s[e], c, g[e] * w[e]), d[e]);
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + off + (size_t)i * 16) = pack16<DT>(d);
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + off + (size_t)i * 16) = grad16<DT>(sr[j], gr[j], dr[j], w, rstd, c);
     }
   }
   if (a.dweight) {
@@ -294,6 +326,112 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
         for (int e = 0; e < N; e += 4) p[e / 4] = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
       }
     }
+  }
+}
+
+// Narrow rows (up to 128 16-byte vectors): a warp per row, NV vectors a lane, no
+// barrier and no ring; many warps keep memory busy. With a CTA per row the gradient
+// of m8039 h272 took 29 us, most of it barriers.
+constexpr int kRowWarps = 8;
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <int DT, bool E4M3, int NV>
+__global__ void __launch_bounds__(32 * kRowWarps) norm_rows_kernel(NormArgs a) {
+  constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
+  const int lane = threadIdx.x & 31, nvec = a.H / N;
+  for (long long r = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); r < a.M; r += (long long)gridDim.x * kRowWarps) {
+    const size_t off = (size_t)r * a.H * es;
+    float v[NV][N];
+    uint4 wr[NV], dr[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + j * 32;
+      if (i >= nvec) continue;
+      Vec16<DT>::load(static_cast<const char*>(a.x) + off + (size_t)i * 16, v[j]);
+      if (a.delta) dr[j] = load_raw(static_cast<const char*>(a.delta) + off + (size_t)i * 16);
+      wr[j] = load_raw(static_cast<const char*>(a.weight) + (size_t)i * 16);
+    }
+    float ss = 0.f, mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (lane + j * 32 >= nvec) continue;
+      if (a.delta) {
+        float d[N];
+        unpack16<DT>(dr[j], d);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[j][e] += d[e];
+      }
+      add_row<DT, E4M3>(v[j], wr[j], ss, mx);
+    }
+    ss = warp_sum(ss);
+    if (E4M3) mx = warp_max_nan(mx);
+    const float2 k = row_factors<E4M3>(a, r, ss, mx, lane == 0);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane + j * 32 < nvec) write_row<DT, E4M3>(a, r, lane + j * 32, v[j], wr[j], k);
+  }
+}
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(32 * kRowWarps) norm_grad_rows_kernel(NormGradArgs a) {
+  constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
+  __shared__ float sums[kRowWarps][NV * 32 * N];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = a.H / N;
+  float dw[NV][N];
+  uint4 wr[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (lane + j * 32 < nvec) wr[j] = load_raw(static_cast<const char*>(a.weight) + (size_t)(lane + j * 32) * 16);
+#pragma unroll
+    for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+  }
+  for (long long r = (long long)blockIdx.x * kRowWarps + warp; r < a.M; r += (long long)gridDim.x * kRowWarps) {
+    const size_t off = (size_t)r * a.H * es;
+    const float rstd = __ldg(a.rstd + r);
+    uint4 sr[NV], gr[NV], dr[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + j * 32;
+      if (i >= nvec) continue;
+      sr[j] = load_raw(static_cast<const char*>(a.s) + off + (size_t)i * 16);
+      gr[j] = load_raw(static_cast<const char*>(a.dy) + off + (size_t)i * 16);
+      dr[j] = a.dsum ? load_raw(static_cast<const char*>(a.dsum) + off + (size_t)i * 16) : make_uint4(0, 0, 0, 0);
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (lane + j * 32 >= nvec) continue;
+      float w[N];
+      unpack16<DT>(wr[j], w);
+      add_grad<DT>(sr[j], gr[j], w, rstd, dw[j], dot);
+    }
+    dot = warp_sum(dot);
+    const float c = rstd * rstd * (dot / (float)a.H);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + j * 32;
+      if (i >= nvec) continue;
+      float w[N];
+      unpack16<DT>(wr[j], w);
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + off + (size_t)i * 16) = grad16<DT>(sr[j], gr[j], dr[j], w, rstd, c);
+    }
+  }
+  if (!a.dweight) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e) sums[warp][(lane + j * 32) * N + e] = dw[j][e];
+  __syncthreads();
+  for (int h = threadIdx.x; h < a.H; h += 32 * kRowWarps) {
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < kRowWarps; ++q) t += sums[q][h];
+    a.partial[(size_t)blockIdx.x * a.H + h] = t;
   }
 }
 
@@ -348,8 +486,17 @@ cudaError_t launch(Kern kern, const Args& a, const Cut& c, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Rows of up to 128 vectors: enough CTAs of 8 rows for eight on every SM.
+inline int row_blocks(int M, int most) { return min((M + kRowWarps - 1) / kRowWarps, most); }
+
 template <int DT, bool E4M3>
 cudaError_t norm_pick(const NormArgs& a, cudaStream_t s) {
+  const int nvec = a.H / Vec16<DT>::N;
+  if (nvec <= 128) {
+    auto kern = nvec <= 32 ? norm_rows_kernel<DT, E4M3, 1> : nvec <= 64 ? norm_rows_kernel<DT, E4M3, 2> : norm_rows_kernel<DT, E4M3, 4>;
+    kern<<<row_blocks(a.M, 8 * 148), 32 * kRowWarps, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   const Cut c = make_cut(a.M, a.H, DT, 2, 2);
   switch (c.nv) {
     case 1: return launch(norm_kernel<DT, E4M3, 1>, a, c, s);
@@ -365,18 +512,31 @@ template <int DT>
 cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
   Cut c = make_cut(a.M, a.H, DT, 3, 1);
   c.blocks = min(c.blocks, kNormGradBlocks);
+  NormGradArgs b = a;
   cudaError_t e;
+  const int nvec = a.H / Vec16<DT>::N;
+  if (nvec <= 128) {
+    c.blocks = row_blocks(a.M, kNormGradBlocks);
+    if (c.blocks == 1) b.partial = a.dweight;  // one CTA's sums are the result
+    auto kern = nvec <= 32 ? norm_grad_rows_kernel<DT, 1> : nvec <= 64 ? norm_grad_rows_kernel<DT, 2> : norm_grad_rows_kernel<DT, 4>;
+    kern<<<c.blocks, 32 * kRowWarps, 0, s>>>(b);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && a.dweight && c.blocks > 1) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
+    return e;
+  }
+  // (dweight may be aligned to 4 bytes only, the wide kernels store 16 at a time)
+  if (c.blocks == 1 && (reinterpret_cast<uintptr_t>(a.dweight) & 15) == 0) b.partial = a.dweight;
   switch (c.nv) {
-    case 1: e = launch(norm_grad_kernel<DT, 1>, a, c, s); break;
-    case 2: e = launch(norm_grad_kernel<DT, 2>, a, c, s); break;
-    case 4: e = launch(norm_grad_kernel<DT, 4>, a, c, s); break;
+    case 1: e = launch(norm_grad_kernel<DT, 1>, b, c, s); break;
+    case 2: e = launch(norm_grad_kernel<DT, 2>, b, c, s); break;
+    case 4: e = launch(norm_grad_kernel<DT, 4>, b, c, s); break;
     default:
       if constexpr (DT == DSPARK_F32)
-        e = launch(norm_grad_kernel<DT, 8>, a, c, s);
+        e = launch(norm_grad_kernel<DT, 8>, b, c, s);
       else
         e = cudaErrorInvalidValue;
   }
-  if (e == cudaSuccess && a.dweight) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
+  if (e == cudaSuccess && a.dweight && b.partial != a.dweight) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
   return e;
 }
 
