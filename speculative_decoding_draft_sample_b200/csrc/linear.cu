@@ -112,11 +112,19 @@ __device__ __forceinline__ void activate(float* v, int act) {
 }
 
 // fp32 outputs (and 2-byte rows that are not whole 16-byte vectors): 16 columns
-// of one lane straight to memory, 32 neighbouring outputs per warp and store. All
-// loads come before the first store: a load behind a store that might alias it
-// waits for its turn. at: column 0; n columns.
+// of one lane straight to memory, 32 neighbouring outputs per warp and store. at:
+// column 0; n columns. Residuals come as bits, loaded a chunk ahead: a load behind
+// a store that might alias it would wait for its turn.
 template <int DT>
-__device__ __forceinline__ void direct16(const Gemm& g, float* v, long long at, int n) {
+__device__ __forceinline__ void direct_load16(const Gemm& g, uint32_t* res, long long at, int n) {
+  using T = typename Elem<DT>::T;
+  const T* p = static_cast<const T*>(g.residual) + at;
+#pragma unroll
+  for (int j = 0; j < 16; ++j, p += g.F)
+    if (j < n) res[j] = DT == DSPARK_F32 ? __float_as_uint((float)*p) : (uint32_t)*p;
+}
+template <int DT>
+__device__ __forceinline__ void direct16(const Gemm& g, float* v, const uint32_t* res, long long at, int n) {
   using T = typename Elem<DT>::T;
   if (g.pre) {
     T* p = static_cast<T*>(g.pre) + at;
@@ -126,14 +134,9 @@ __device__ __forceinline__ void direct16(const Gemm& g, float* v, long long at, 
   }
   activate<16>(v, g.act);
   if (g.residual) {
-    const T* p = static_cast<const T*>(g.residual) + at;
-    T res[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j, p += g.F)
-      if (j < n) res[j] = *p;
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (j < n) v[j] += Elem<DT>::to_float(res[j]);
+      if (j < n) v[j] += __uint_as_float(DT == DSPARK_F32 ? res[j] : res[j] << 16);
   }
   T* p = static_cast<T*>(g.out) + at;
 #pragma unroll
@@ -149,23 +152,29 @@ __device__ __forceinline__ void direct16(const Gemm& g, float* v, long long at, 
 __device__ __forceinline__ uint32_t stage_at(int r, int q) { return r * 64 + ((q ^ ((r >> 1) & 3)) << 4); }
 
 // Moves rows between a warp's stage and memory (p: token t0, the warp's first
-// feature; nf features of the row remain): 8 rows x 64 bytes an instruction.
-template <bool STORE>
-__device__ __forceinline__ void move_rows(unsigned char* stage, uint16_t* p, int F, int nf, int rows, int lane) {
+// feature; nf features of the row remain): 8 rows x 64 bytes an instruction. Loads
+// go through registers, so that they can be started long before.
+__device__ __forceinline__ void load_rows(uint4* x, const uint16_t* p, int F, int nf, int rows, int lane) {
+  const int q = lane & 3;
+  if (q * 8 >= nf) return;
+  p += (long long)(lane >> 2) * F + q * 8;
+#pragma unroll
+  for (int i = 0; i < kChunk / 8; ++i)
+    if (i * 8 + (lane >> 2) < rows) x[i] = *reinterpret_cast<const uint4*>(p + (long long)(i * 8) * F);
+}
+__device__ __forceinline__ void stage_rows(unsigned char* stage, const uint4* x, int lane) {
+#pragma unroll
+  for (int i = 0; i < kChunk / 8; ++i)
+    *reinterpret_cast<uint4*>(stage + stage_at(i * 8 + (lane >> 2), lane & 3)) = x[i];
+}
+__device__ __forceinline__ void store_rows(const unsigned char* stage, uint16_t* p, int F, int nf, int rows, int lane) {
   const int q = lane & 3;
   if (q * 8 >= nf) return;
   p += (long long)(lane >> 2) * F + q * 8;
 #pragma unroll
   for (int i = 0; i < kChunk / 8; ++i) {
     const int r = i * 8 + (lane >> 2);
-    if (r < rows) {
-      uint4* s = reinterpret_cast<uint4*>(stage + stage_at(r, q));
-      uint4* d = reinterpret_cast<uint4*>(p + (long long)(i * 8) * F);
-      if (STORE)
-        *d = *s;
-      else
-        *s = *d;
-    }
+    if (r < rows) *reinterpret_cast<uint4*>(p + (long long)(i * 8) * F) = *reinterpret_cast<const uint4*>(stage + stage_at(r, q));
   }
 }
 
@@ -391,8 +400,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = STAGED ? quarter * 32 + (lane >> 2) : ln;
     float ls[kRows], bias[kRows];
 
+    // the residual of columns c .. c + kCols - 1, in the layout that finish() takes
+    struct Residual {
+      uint4 x[4];
+    };
+    auto load_residual = [&](Residual& res, int f0, int t0, int c) {
+      const int cols = min(min(kCols, g.nt - c), g.T - t0 - c);
+      if constexpr (STAGED) {
+        const int fw = f0 + quarter * 32;
+        load_rows(res.x, static_cast<const uint16_t*>(g.residual) + (long long)(t0 + c) * g.F + fw, g.F, g.F - fw, cols, lane);
+      } else {
+        const int n = f0 + ln < g.F ? cols : 0;
+        const long long at = (long long)(t0 + c) * g.F + f0 + ln;
+        uint32_t* bits = reinterpret_cast<uint32_t*>(res.x);
+        if (g.out_type == DSPARK_F32)
+          direct_load16<DSPARK_F32>(g, bits, at, n);
+        else
+          direct_load16<DSPARK_BF16>(g, bits, at, n);
+      }
+    };
+
     // columns c .. c + kCols - 1 of the tile to the outputs; cscale: lane j's is column j's scale
-    auto finish = [&](float* v, int f0, int t0, int c, float cscale) {
+    auto finish = [&](float* v, const Residual& res, int f0, int t0, int c, float cscale) {
       const int cols = min(min(kCols, g.nt - c), g.T - t0 - c);
       if constexpr (!STAGED) {
         if (g.lane_scale) {
@@ -406,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = f0 + ln < g.F ? cols : 0;
         const long long at = (long long)(t0 + c) * g.F + f0 + ln;
         if (g.out_type == DSPARK_F32)
-          direct16<DSPARK_F32>(g, v, at, n);
+          direct16<DSPARK_F32>(g, v, reinterpret_cast<const uint32_t*>(res.x), at, n);
         else
-          direct16<DSPARK_BF16>(g, v, at, n);
+          direct16<DSPARK_BF16>(g, v, reinterpret_cast<const uint32_t*>(res.x), at, n);
       } else {
         if (g.lane_scale) {
 #pragma unroll
@@ -439,14 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_matrix_t(mat + k * 512, q);
           }
           __syncwarp();
-          move_rows<true>(stage, static_cast<uint16_t*>(p) + at, g.F, g.F - fw, cols, lane);
+          store_rows(stage, static_cast<uint16_t*>(p) + at, g.F, g.F - fw, cols, lane);
           __syncwarp();  // the stage is free again
         };
         if (g.pre) put(g.pre);
         activate<kCols>(v, g.act);
         if (g.residual) {
-          move_rows<false>(stage, const_cast<uint16_t*>(static_cast<const uint16_t*>(g.residual)) + at, g.F, g.F - fw, cols,
-                           lane);
+          stage_rows(stage, res.x, lane);
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -465,8 +493,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
 
+    // A tile's residual (64 KB) is asked into L2 while the tile before is worked on:
+    // a warp's own loads hold too few bytes to cover memory's latency.
+    auto prefetch_residual = [&](const Tiles& at) {
+      const int f0 = at.tf * kTileF + rank * kLanes, t = tid - 64, t0 = at.tt * g.nt;
+      if (!at.more() || t >= g.nt || t0 + t >= g.T || f0 >= g.F) return;
+      const int es = g.out_type == DSPARK_F32 ? 4 : 2, bytes = min(kLanes, g.F - f0) * es;
+      const char* row = static_cast<const char*>(g.residual) + ((long long)(t0 + t) * g.F + f0) * es;
+      for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + bytes - 1));
+    };
+    if (g.residual) prefetch_residual(w);
+
     uint32_t buf = 0, aph = 0;
     for (; w.more(); w.next(g)) {
+      if (g.residual) {
+        Tiles after = w;
+        after.next(g);
+        prefetch_residual(after);
+      }
       const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
@@ -474,6 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ls[i] = g.lane_scale && f < g.F ? __ldg(g.lane_scale + f) : 0.f;
         bias[i] = g.bias && f < g.F ? __ldg(g.bias + f) : 0.f;
       }
+      const int c1 = min(g.nt, g.T - t0);
+      Residual next = {};
+      if (g.residual && group * kCols < c1) load_residual(next, f0, t0, group * kCols);
       bool ok = !*dead;
       if (ok && !mbar_wait(&acc_full[buf], aph)) {
         ok = false;
@@ -483,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
-      const int c1 = min(g.nt, g.T - t0);
       for (int c = group * kCols; c < c1; c += kStep) {
         float v[kCols];
         const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
@@ -505,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[j] += s[j * kLanes + ln];
           }
         }
-        finish(v, f0, t0, c, cscale);
+        const Residual res = next;
+        if (g.residual && c + kStep < c1) load_residual(next, f0, t0, c + kStep);
+        finish(v, res, f0, t0, c, cscale);
       }
       if (group * kCols >= c1 && lane == 0) mbar_arrive_relaxed(acc_free + 8 * buf);  // nothing to read
       buf ^= 1;
