@@ -493,7 +493,8 @@ int dspark_residual_norm_grad(const void* s, const void* weight, const float* rs
  *   x [M, K], w [N, K] in_type (DSPARK_BF16 or DSPARK_E4M3)
  *   x_scale [M], w_scale [N] f32 (both with DSPARK_E4M3, both NULL with DSPARK_BF16)
  *   bias [N] f32 or NULL; residual [M, N] out_type or NULL (it may be y)
- *   y [M, N] out_type (DSPARK_F32 or DSPARK_BF16) out; pre [M, N] out_type out or NULL (for the gradient)
+ *   y [M, N] out_type (DSPARK_F32 or DSPARK_BF16) out; pre [M, N] out_type out or NULL (for the
+ *     gradient). Neither may overlap another tensor, but for residual == y.
  *   act DSPARK_ACT_*
  * Limits: 1 <= M, N < 2^24, 1 <= K < 2^20, K a multiple of 16 bytes (8 bf16, 16
  * e4m3 entries); x and w 16-byte aligned, y, pre and residual aligned to their

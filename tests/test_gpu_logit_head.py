@@ -212,3 +212,121 @@ def test_heads_refuse_what_does_not_fit(cuda_ok):
     rnd = SpecRound(4, 2, 512, 64)
     with pytest.raises(bn.DSparkError, match="vocabulary"):
         rnd.run({"target_hidden": hidden(g, 4, 3)}, SEED, 0, target_head=head)
+
+
+def test_calls_at_once_on_two_streams(cuda_ok):
+    """Every operator on two streams at the same time, each with its own workspace."""
+    V, M = 20000, 40
+    norm_w, w, g = parts(V, seed=9)
+    xs = [hidden(g, M) for _ in range(2)]
+    toks = [torch.randint(0, V, (M, 1), generator=g, device="cuda", dtype=torch.int32) for _ in range(2)]
+
+    def issue(i, stream, bufs):
+        head, scores, logits, dlogits, dx = bufs
+        head.run(xs[i], logits, stream=stream)
+        rows = logits.view(M, 1, V)
+        scores.run(rows, toks[i], None, stream=stream)
+        scores.gradient(rows, toks[i], None, torch.ones_like(scores.logp), dlogits, stream=stream)
+        head.gradient(dlogits, dx, stream=stream)
+
+    def buffers():
+        return (LogitHead(norm_w, w, M), TokenScores(M, 1, V, 5), torch.empty(M, V, device="cuda", dtype=BF16),
+                torch.empty(M, 1, V, device="cuda", dtype=BF16), torch.empty(M, H, device="cuda", dtype=BF16))
+
+    want = []
+    for i in range(2):
+        b = buffers()
+        issue(i, None, b)
+        want.append((b[1].logp, b[1].top_idx, b[4]))
+    streams, bufs = [torch.cuda.Stream() for _ in range(2)], [buffers() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            issue(i, streams[i], bufs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        got = (bufs[i][1].logp, bufs[i][1].top_idx, bufs[i][4])
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        assert bufs[i][0].status() == (0, -1) and bufs[i][1].status() == (0, -1)
+
+
+def test_offsets_past_32_bits(cuda_ok):
+    """More than 2^31 entries in a tensor: the last rows against the same rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    B, V, n = 16500, 131072, 6              # 2.16e9 logits
+    few = torch.randn(n, 1, V, generator=g, device="cuda").to(BF16)
+    logits = torch.empty(B, 1, V, device="cuda", dtype=BF16)
+    logits[-n:] = few
+    tok = torch.full((B, 1), -1, device="cuda", dtype=torch.int32)
+    tok[-n:] = torch.randint(0, V, (n, 1), generator=g, device="cuda", dtype=torch.int32)
+    many, alone = TokenScores(B, 1, V, 3), TokenScores(n, 1, V, 3)
+    many.run(logits, tok, None)
+    alone.run(few, tok[-n:].contiguous(), None)
+    # a row shared by a cluster adds its sums in another order than a CTA of its own
+    assert (many.logp[-n:] - alone.logp).abs().max().item() <= 2.0 ** -24 * (V / 256 + 16) * 2 + 2.0 ** -20
+    assert torch.equal(many.top_idx[-n:], alone.top_idx) and bool((many.logp[:-n] == 0).all())
+    ones = torch.ones(B, 1, device="cuda")
+    many.gradient(logits, tok, None, ones, logits)
+    d = torch.empty_like(few)
+    bn.token_logprobs_grad(few, tok[-n:].contiguous(), None, many.lse[-n:].contiguous(), ones[-n:].contiguous(), d, alone.ws)
+    assert torch.equal(logits[-n:], d) and bool((logits[0] == 0).all())
+
+    K = 64                                  # the same buffer as a product's output
+    x, w = torch.randn(B, K, generator=g, device="cuda").to(BF16), torch.randn(V, K, generator=g, device="cuda").to(BF16)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    bn.linear(x, w, logits.view(B, V), ws)
+    want = x[-n:].double() @ w.double().t()
+    S = x[-n:].double().abs() @ w.double().abs().t()
+    err = (logits.view(B, V)[-n:].double() - want).abs()
+    assert bool((err <= 2.0 ** -8 * want.abs() + 2.0 ** -23 * (K / 16 + 156) * S).all())
+
+    M, W = 131500, 16384                    # and as rows of a norm, in place
+    rows = logits.view(-1)[:M * W].view(M, W)
+    last = torch.randn(n, W, generator=g, device="cuda").to(BF16)
+    rows[-n:] = last
+    weight = torch.ones(W, device="cuda", dtype=BF16)
+    rstd = torch.empty(M, device="cuda")
+    y = torch.empty(M, W, device="cuda", dtype=torch.float8_e4m3fn)
+    scale = torch.empty(M, device="cuda")
+    nws = torch.zeros(bn.workspace_bytes(bn.OP_NORM, M, 0, W, 0, 0), dtype=torch.uint8, device="cuda")
+    bn.residual_norm(rows, rows, weight, 1e-6, y, nws, sum=rows, y_scale=scale, rstd=rstd)
+    v = 2 * last.double()
+    exact = v / torch.sqrt(v.square().mean(1, keepdim=True) + 1e-6)
+    tol = (2.0 ** -4 + 2.0 ** -16) * exact.abs() + 2.0 ** -10 * scale[-n:, None].double()
+    assert bool(((y[-n:].double() * scale[-n:, None].double() - exact).abs() <= tol).all())
+    assert torch.equal(rows[-n:], 2 * last)
+
+
+def test_misaligned_tensors_are_refused(cuda_ok):
+    def off(shape, dtype):
+        n = 1
+        for s in shape:
+            n *= s
+        return torch.zeros(n + 8, device="cuda", dtype=dtype)[1:1 + n].view(shape)
+
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    b = lambda *s: torch.zeros(*s, device="cuda", dtype=BF16)  # noqa: E731
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    tok = torch.zeros(2, 2, device="cuda", dtype=torch.int32)
+    calls = [
+        lambda: bn.token_logprobs(off((2, 2, 64), BF16), tok, None, f(2, 2), ws),
+        lambda: bn.token_logprobs_grad(b(2, 2, 64), tok, None, f(2, 2), f(2, 2), off((2, 2, 64), BF16), ws),
+        lambda: bn.residual_norm(off((4, 64), BF16), None, b(64), 1e-6, b(4, 64), ws),
+        lambda: bn.residual_norm(b(4, 64), None, b(64), 1e-6, off((4, 64), BF16), ws),
+        lambda: bn.residual_norm_grad(b(4, 64), b(64), f(4), off((4, 64), BF16), b(4, 64), ws),
+        lambda: bn.linear(off((4, 64), BF16), b(8, 64), b(4, 8), ws),
+        lambda: bn.linear(b(4, 64), off((8, 64), BF16), b(4, 8), ws),
+        lambda: bn.linear_grad(b(4, 64), b(8, 64), off((4, 8), BF16), ws, dx=b(4, 64)),
+        lambda: bn.linear_grad(b(4, 64), b(8, 64), b(4, 8), ws, dx=off((4, 64), BF16)),
+        lambda: bn.linear(b(4, 64), b(8, 64), b(4, 8), off((256,), torch.uint8)),
+    ]
+    for call in calls:
+        with pytest.raises(bn.DSparkError, match="invalid argument"):
+            call()
+    for call in (lambda: bn.residual_norm(b(4, 60), None, b(60), 1e-6, b(4, 60), ws),
+                 lambda: bn.linear(b(4, 60), b(8, 60), b(4, 8), ws),
+                 lambda: bn.linear(b(0, 64), b(8, 64), b(0, 8), ws),
+                 lambda: bn.linear_grad(b(4, 64), b(12, 64), b(4, 12), ws, dx=b(4, 64)),
+                 lambda: bn.token_logprobs(b(2, 2, 60), tok, None, f(2, 2), ws)):
+        with pytest.raises(bn.DSparkError, match="invalid argument"):
+            call()
