@@ -21,10 +21,11 @@
 // Alternatives: a thread reads a fixed column of the row's 16-byte vectors and
 // knows its column's largest entry. The n largest entries of the slice all lie
 // in the columns with the n largest maxima, at or above the n-th of those maxima.
-// One warp finds a value that n to n + 8 maxima reach by bisection; only these
-// columns are read a second time (out of L2) and the few entries that pass are
-// ranked by counting. Where equal maxima leave more than n + 8, the columns are
-// chosen by 64-bit keys (value, then lowest index). Candidates are always ranked
+// One warp finds a value that n to n + 8 maxima reach by bisection; of these
+// columns the segments (up to 8 in a column) whose own maxima reach it are read a
+// second time, out of L2, and the few entries that pass are ranked by counting.
+// Where equal maxima leave more than n + 8 columns, they are chosen by 64-bit keys
+// (value, then lowest index). Candidates are always ranked
 // by these keys, which are unique, so neither ties nor the order of the list's
 // atomics change a result.
 #include <climits>
@@ -53,6 +54,8 @@ constexpr int kSlots = 2;        // ring of 16 KB slots: with four CTAs on an SM
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCluster = 8;   // CTAs that share a row
 constexpr int kCand = 1024;      // candidate list; a slice with more takes the selection loop
+constexpr int kSegs = 8;         // segments of a column with a maximum of their own, at most
+constexpr int kUnits = 256;      // list of segments to read again; where it is full, whole columns are read
 constexpr int kSlack = 8;        // columns that the bisection may take beyond n
 constexpr float kFloorZ = -150.f;
 constexpr float kClampZ = 200.f;
@@ -196,12 +199,15 @@ struct Shared {
   RowStat cta_stat[kMaxCluster];                     // CTA 0: every CTA's statistics
   unsigned long long lists[kMaxCluster * kMaxTop];   // CTA 0: every CTA's n largest keys
   uint32_t vals[kThreads];                           // the columns' largest values (value_key), 0 = no entry
+  float seg_max[kSegs][kThreads];                    // the columns' segments' largest values
   unsigned long long keys[kThreads];                 // the same as full keys, where values tie
   unsigned long long cand[kCand];
   unsigned long long red[kThreads / 32];
   unsigned long long thr;                            // the bound
   int sel[kMaxTop + kSlack];                         // the columns that reach it
   int nsel, ncand;
+  int units[kUnits];                                 // (segment, column) pairs to read again
+  int nunit;
   int ties;                                          // equal maxima left too many columns
   int dead;                                          // a bounded wait gave up
 };
@@ -263,13 +269,14 @@ __device__ void select_columns(Shared& sh, int n, int lane) {
     sh.thr = (unsigned long long)bound << 32;
     sh.ties = !ok;
     sh.ncand = 0;
+    sh.nunit = 0;
   }
 }
 
 // The entries of this CTA's slice [v0, v1) (vectors) that may be among its n
 // largest, in sh.cand (sh.ncand of them; more than kCand where the list is full).
 template <int DT>
-__device__ void slice_candidates(Shared& sh, const char* row, int v0, int v1, float mv, int mi, int n) {
+__device__ void slice_candidates(Shared& sh, const char* row, int v0, int v1, int segs, int seg_slots, float mv, int mi, int n) {
   constexpr int N = Vec16<DT>::N;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sh.ties) {  // full keys: the first entry equal to the maximum, in the slot where it appeared
@@ -297,8 +304,18 @@ __device__ void slice_candidates(Shared& sh, const char* row, int v0, int v1, fl
   }
   const unsigned long long thr = sh.thr;
   const float floor = key_value(thr);
-  const int per = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a column
-  const int total = sh.nsel * per;
+  for (int u = tid; u < sh.nsel * segs; u += kThreads) {
+    const int col = sh.sel[u / segs], seg = u % segs;
+    if (!(sh.seg_max[seg][col] < floor)) {
+      const int c = atomicAdd(&sh.nunit, 1);
+      if (c < kUnits) sh.units[c] = seg * kThreads + col;
+    }
+  }
+  readers_sync();
+  // vectors of a unit: every kThreads-th of its segment
+  const bool listed = sh.nunit <= kUnits;
+  const int per = listed ? seg_slots * kUnroll : (v1 - v0 + kThreads - 1) / kThreads;
+  const int total = (listed ? sh.nunit : sh.nsel) * per;
   for (int q0 = tid; q0 < total; q0 += 4 * kThreads) {
     uint4 w[4];
     int at[4];
@@ -306,7 +323,10 @@ __device__ void slice_candidates(Shared& sh, const char* row, int v0, int v1, fl
     for (int j = 0; j < 4; ++j) {
       const int q = q0 + j * kThreads;
       at[j] = v1;
-      if (q < total) at[j] = v0 + sh.sel[q / per] + (q % per) * kThreads;
+      if (q < total) {
+        const int u = listed ? sh.units[q / per] : sh.sel[q / per];
+        at[j] = v0 + u % kThreads + (u / kThreads * seg_slots * kUnroll + q % per) * kThreads;
+      }
       if (at[j] < v1) w[j] = *reinterpret_cast<const uint4*>(row + (size_t)at[j] * 16);
     }
 #pragma unroll
@@ -484,12 +504,24 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   uint32_t low = W::floor_of(-reach);
   int mi = v0 + tid;
 
-  auto batch = [&](uint32_t (&v)[kUnroll][4], int i) {
+  const int seg_slots = (chunks + kSegs - 1) / kSegs, segs = (chunks + seg_slots - 1) / seg_slots;
+  float seg_m = -INFINITY;  // of the current segment, with seg_left slots to come
+  int seg = 0, seg_left = seg_slots;
+
+  auto batch = [&](uint32_t (&v)[kUnroll][4], int i, bool last) {
     uint32_t b2[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) b2[e] = W::max_nan(W::max_nan(v[0][e], v[1][e]), W::max_nan(v[2][e], v[3][e]));
     const float bm = W::top(W::max_nan(W::max_nan(b2[0], b2[1]), W::max_nan(b2[2], b2[3])));
     st.chk = max_nan(st.chk, bm);
+    if (n) {
+      seg_m = fmaxf(seg_m, bm);
+      if (--seg_left == 0 || last) {
+        sh.seg_max[seg++][tid] = seg_m;
+        seg_m = -INFINITY;
+        seg_left = seg_slots;
+      }
+    }
     if (bm > st.m) {
       // a maximum of the size of the type's lowest value adds nothing here: another
       // column's is larger, or the row takes the plain pass
@@ -554,7 +586,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
       }
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&sh.empty[slot])) : "memory");
-      batch(v, i);
+      batch(v, i, c + 1 == chunks);
       if (++slot == kSlots) {
         slot = 0;
         ph ^= 1;
@@ -596,7 +628,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
       root->cta_stat[q] = c;
     }
     readers_sync();
-    if (n) slice_candidates<DT>(sh, row, v0, v1, mv, mv_i, n);
+    if (n) slice_candidates<DT>(sh, row, v0, v1, segs, seg_slots, mv, mv_i, n);
     if (n && C > 1) slice_top<DT>(sh, row, v0, v1, n, [&](int rank, unsigned long long k) { root->lists[q * n + rank] = k; });
   }
   if (C > 1) cluster.sync();
