@@ -28,6 +28,9 @@
 // the contraction; the other pairs leave their fp32 sums in the first one's shared
 // memory (its ring is free by then), which adds them in the order of the parts and
 // finishes the tile.
+// Measured (short runs): m1536 n129280 k4096 1090 us in bf16 (1.49 PFLOP/s), 549 us in
+// e4m3 (2.96 PFLOP/s); m16 n129280 k4096 165 us (6.4 TB/s, memory bounds it); gradient
+// m2048 n5120 k4096 143 us.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
 #include "host.cuh"
 #include "linear.cuh"

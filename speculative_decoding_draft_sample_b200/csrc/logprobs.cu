@@ -28,6 +28,10 @@
 // (value, then lowest index). Candidates are always ranked
 // by these keys, which are unique, so neither ties nor the order of the list's
 // atomics change a result.
+//
+// Measured: b256 j6 v129280 with 42 % of the rows padded away and 5 alternatives 59 us
+// (3.9 TB/s; 54 without alternatives, 49 with neither exponentials nor alternatives);
+// b64 j6 v151936 in fp32 48 us (4.9 TB/s).
 #include <climits>
 
 #include <cooperative_groups.h>
