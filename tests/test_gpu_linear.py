@@ -236,3 +236,37 @@ def test_captured_shared_workspace_and_side_stream(cuda_ok):
             graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, want) and torch.equal(b, want.roll(1, 0))
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 1456, 1640), (300, 1000, 520), (1000, 4096, 1024)])
+def test_gradient_captured_and_followed(cuda_ok, M, N, K):
+    """dx and dw run beside each other; what follows in the stream sees both complete."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, _ = operand(M, K, False, g)
+    w, _ = operand(N, K, False, g, K ** -0.5)
+    dy = torch.randn(M, N, generator=g, device="cuda").to(BF16)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device="cuda")
+    ws = workspace(M, N, K, mode=1)
+    copies = [torch.empty_like(t) for t in (dx, dw, db)]
+
+    def step():
+        bn.linear_grad(x, w, dy, ws, dx=dx, dw=dw, dbias=db, pre=dy, act="silu")
+        for c, t in zip(copies, (dx, dw, db)):
+            c.copy_(t)
+
+    step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (dx, dw, db)]
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        step()
+    for run_once in (step, graph.replay, graph.replay, step):
+        for t in (dx, dw, db, *copies):
+            t.fill_(7)
+        run_once()
+        torch.cuda.synchronize()
+        for a, b, c in zip(copies, want, (dx, dw, db)):
+            assert torch.equal(a, b) and torch.equal(c, b)
+    assert bn.read_status(ws) == (0, -1)
