@@ -206,7 +206,8 @@ class SpecRound:
         if tuple(hidden.shape) != (self.B, J, head.H):
             raise bn.DSparkError(f"{name}_hidden must have shape {(self.B, J, head.H)}, got {tuple(hidden.shape)}")
         if out is None:
-            out = torch.empty((self.B, J, self.V), dtype=self.dtype, device=self.x.device)
+            with torch.cuda.stream(stream):  # memory that this stream's work, not another's, may still use
+                out = torch.empty((self.B, J, self.V), dtype=self.dtype, device=self.x.device)
         head.run(hidden, out, delta=inp.get(name + "_delta"), stream=stream)
         return out
 
@@ -219,7 +220,8 @@ class SpecRound:
         if self.verified is None:
             raise bn.DSparkError("score() needs a run() before it")
         if self.scores is None or (0 if self.scores.top_idx is None else self.scores.top_idx.shape[2]) != n_top:
-            self.scores = TokenScores(self.B, self.K + 1, self.V, n_top, self.dtype, self.x.device)
+            with torch.cuda.stream(stream):  # the workspace is cleared in order with the call
+                self.scores = TokenScores(self.B, self.K + 1, self.V, n_top, self.dtype, self.x.device)
         self.scores.run(self.verified, self.out, temp, stream=stream)
         return self.scores
 

@@ -330,3 +330,33 @@ def test_misaligned_tensors_are_refused(cuda_ok):
                  lambda: bn.token_logprobs(b(2, 2, 60), tok, None, f(2, 2), ws)):
         with pytest.raises(bn.DSparkError, match="invalid argument"):
             call()
+
+
+def test_buffers_made_by_a_call_belong_to_its_stream(cuda_ok):
+    """run() and score() make their logits and scores at first use; neither the memory's last
+    user on the current stream nor its own clearing may come behind the call's work."""
+    w, host, th, dh = round_inputs()
+    dev = to_device(host)
+    side = torch.cuda.Stream()
+    plain = SpecRound(w.B, w.K, w.V, w.r)
+    plain.run(dev, SEED, 3, target_head=th, draft_head=dh)
+    bad = dev["temp"].clone()
+    bad[1] = -1
+    want = plain.score(bad, n_top=2)
+    assert want.status()[0] == bn.STATUS_BAD_TEMP
+    rnd = SpecRound(w.B, w.K, w.V, w.r)
+    old = [torch.empty_like(plain.target), torch.empty_like(plain.base)]
+    for t in old:
+        t.fill_(0)  # (the kernel is loaded now, not behind the sleep)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(500_000_000)  # a quarter of a second; the current stream is still busy with the memory it frees
+    for t in old:
+        t.fill_(7)
+    del t, old
+    rnd.run(dev, SEED, 3, stream=side, target_head=th, draft_head=dh)
+    got = rnd.score(bad, n_top=2, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(rnd.target, plain.target) and torch.equal(rnd.base, plain.base)
+    assert torch.equal(got.logp, want.logp) and torch.equal(rnd.out, plain.out)
+    assert got.status() == (bn.STATUS_BAD_TEMP, 1)
