@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   uint32_t low = W::floor_of(-reach);
   int mi = v0 + tid;
 
-  const int seg_slots = (chunks + kSegs - 1) / kSegs, segs = (chunks + seg_slots - 1) / seg_slots;
+  const int seg_slots = max(1, (chunks + kSegs - 1) / kSegs), segs = (chunks + seg_slots - 1) / seg_slots;
   float seg_m = -INFINITY;  // of the current segment, with seg_left slots to come
   int seg = 0, seg_left = seg_slots;
 
