@@ -518,7 +518,7 @@ int dspark_linear(const void* x, const void* w, const float* x_scale, const floa
  * Limits: those of dspark_linear, and N % 8 == 0; every tensor 16-byte aligned.
  * Outputs must not overlap the inputs.
  * Workspace: dspark_workspace_bytes(DSPARK_OP_LINEAR, M, act ? 1 : 2, N, K,
- * DSPARK_BF16). Up to four launches: dpre, its column sums, dx, dw.
+ * DSPARK_BF16). Up to four launches: dpre, dx, dw, dpre's column sums.
  */
 int dspark_linear_grad(const void* x, const void* w, const void* dy, const void* pre, int M, int N,
                        int K, int act, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,

@@ -765,8 +765,8 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   float* partial = reinterpret_cast<float*>(dpre_buf + (a.act == DSPARK_ACT_NONE ? 0 : round_up((size_t)a.M * a.N * 2, 256)));
   const void* dpre = a.act == DSPARK_ACT_NONE ? a.dy : dpre_buf;
   cudaError_t e;
+  const int runs = dpre_runs(a.M, a.N);
   if (a.act != DSPARK_ACT_NONE || a.dbias) {
-    const int runs = dpre_runs(a.M, a.N);
     const int rows_per = (a.M + runs - 1) / runs;
     if (runs == 1) partial = a.dbias;  // one run's sums are the result
     auto kern = a.act == DSPARK_ACT_RELU   ? dpre_kernel<DSPARK_ACT_RELU>
@@ -776,7 +776,6 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
     kern<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, rows_per, dpre_buf, a.dbias ? partial : nullptr);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.dbias && runs > 1 && (e = column_sums_launch(partial, runs, a.N, a.dbias, s)) != cudaSuccess) return e;
   }
   CUtensorMap ma, mb;
   Gemm g = {};
@@ -798,10 +797,14 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
     g.out = a.dw;
     // dw takes nothing from dx: it starts on the SMs that dx leaves or never used, and
     // waits for dx before it ends (dx, dw and dbias at m5 n1456 k1640 22.7 us, one after
-    // the other 24.6; m1341 n3808 k4984 109 and 116; m2048 n5120 k4096 142.5 and 143.9)
+    // the other 24.6; m1341 n3808 k4984 110 and 116; m2048 n5120 k4096 142.5 and 143.9)
     g.beside = a.dx != nullptr;
     if ((e = gemm_launch<false, true, true, true>(g, pw, ma, mb, s)) != cudaSuccess) return e;
   }
+  // the sums need dpre_kernel's partial ones alone, which are complete where a product runs: they run
+  // beside the last (dx, dw and dbias at m64 n1024 k1024 18.8 us, 22.4 before the products; m300
+  // n2048 k2048 26.6 and 29.0)
+  if (a.dbias && runs > 1) return column_sums_launch(partial, runs, a.N, a.dbias, s, a.dx || a.dw);
   return cudaSuccess;
 }
 

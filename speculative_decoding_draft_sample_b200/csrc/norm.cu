@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) norm_grad_rows_kernel(NormGrad
 // out[h] = sum over the G partial rows: 32 columns a CTA, a warp every 32nd row,
 // four of them in flight (a warp every eighth row one at a time took 7 us for 296
 // rows of 4096, more than twice as long).
-__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int G, int H, float* out) {
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int G, int H, float* out, bool beside) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
@@ -455,6 +455,8 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
   __syncthreads();
   const float t = warp_sum(part[lane][row]);
   if (lane == 0 && blockIdx.x * 32 + row < H) out[blockIdx.x * 32 + row] = t;
+  // what follows in the stream may rely on the launch before being complete too
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // How a call's rows are cut: threads of a block and vectors per thread (the fewest
@@ -542,9 +544,17 @@ cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s) {
-  column_sums_kernel<<<(H + 31) / 32, 1024, 0, s>>>(partial, G, H, out);
-  return cudaGetLastError();
+cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, bool beside) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((H + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, column_sums_kernel, partial, G, H, out, beside);
 }
 
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {

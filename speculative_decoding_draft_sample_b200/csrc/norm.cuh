@@ -38,7 +38,8 @@ constexpr int kNormGradBlocks = 296;
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s);
 cudaError_t norm_grad_launch(const NormGradArgs& a, cudaStream_t s);
 
-// out[h] = sum over g < G of partial[g, h], in a fixed order.
-cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s);
+// out[h] = sum over g < G of partial[g, h], in a fixed order. beside: the launch before
+// in the stream, which touches neither, may still run; the sums wait for it before they end.
+cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, bool beside = false);
 
 }  // namespace dspark
