@@ -69,6 +69,12 @@ enum : unsigned int {  // wait sites recorded when a bounded wait gives up
   kWhereAccEmpty = 43,
 };
 
+// A launch that may start while the one before it in the stream still runs: kBeside
+// shares no output with it and no input that either writes, and waits for it before it
+// ends; kAfter reads what it wrote, and waits when its own barriers and tensor memory
+// are set up.
+enum : int { kAlone, kBeside, kAfter };
+
 struct Gemm {
   int F, T;                 // lanes (contiguous outputs) and columns in all
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
@@ -82,7 +88,7 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  int beside;               // the launch before may still run (it shares no output and no input that either writes)
+  int order;                // kAlone, or against the launch before in the stream: kBeside, kAfter
   Status* status;
 };
 
@@ -256,7 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  // a launch made to run beside this one may start on the SMs that it leaves free
+  if (g.order == kAfter) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // a launch made to run beside this one may start on the SMs that it leaves free (not
+  // before the wait above: it relies on the same results)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // The producer's and the issuer's loop have to keep up with a block of 512
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // neither CTA leaves while the other's arrivals or loads may still reach it
   fence_after();
   // what follows in the stream may rely on the launch before being complete too
-  if (g.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g.order == kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -585,6 +593,7 @@ template <int ACT>
 __global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* pre, int M, int N, int rows_per, void* dpre,
                                                    float* partial) {
   __shared__ float part[kDpreRows][256 + 8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that waits for this kernel sets itself up
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int n0 = blockIdx.x * 256 + lane * 8;
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows_per);
@@ -721,7 +730,7 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = g.beside ? 2 : 1;
+  cfg.numAttrs = g.order == kAlone ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
 }
 
@@ -783,6 +792,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   g.out_type = DSPARK_BF16;
   g.act = DSPARK_ACT_NONE;
   g.status = a.status;
+  if (a.act != DSPARK_ACT_NONE || a.dbias) g.order = kAfter;
   if (a.dx) {  // lanes k, columns m, contraction n
     if (!make_map(&ma, a.w, 2, a.K, a.N, 64) || !make_map(&mb, dpre, 2, a.N, a.M, px.nt / 2)) return cudaErrorInvalidValue;
     g.T = a.M;
@@ -798,7 +808,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
     // dw takes nothing from dx: it starts on the SMs that dx leaves or never used, and
     // waits for dx before it ends (dx, dw and dbias at m5 n1456 k1640 22.7 us, one after
     // the other 24.6; m1341 n3808 k4984 110 and 116; m2048 n5120 k4096 142.5 and 143.9)
-    g.beside = a.dx != nullptr;
+    if (a.dx) g.order = kBeside;
     if ((e = gemm_launch<false, true, true, true>(g, pw, ma, mb, s)) != cudaSuccess) return e;
   }
   // the sums need dpre_kernel's partial ones alone, which are complete where a product runs: they run

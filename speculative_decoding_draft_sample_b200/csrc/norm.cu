@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
     for (int g = row; g < G; g += 128) {
       float d[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = g + 32 * j < G ? partial[(size_t)(g + 32 * j) * H + h] : 0.f;
+      for (int j = 0; j < 4; ++j) d[j] = g + 32 * j < G ? __ldcg(partial + (size_t)(g + 32 * j) * H + h) : 0.f;
       acc += (d[0] + d[1]) + (d[2] + d[3]);
     }
   }
