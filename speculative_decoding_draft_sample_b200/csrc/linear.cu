@@ -69,12 +69,6 @@ enum : unsigned int {  // wait sites recorded when a bounded wait gives up
   kWhereAccEmpty = 43,
 };
 
-// A launch that may start while the one before it in the stream still runs: kBeside
-// shares no output with it and no input that either writes, and waits for it before it
-// ends; kAfter reads what it wrote, and waits when its own barriers and tensor memory
-// are set up.
-enum : int { kAlone, kBeside, kAfter };
-
 struct Gemm {
   int F, T;                 // lanes (contiguous outputs) and columns in all
   int kblocks;              // 128-byte (K-major) or 64-row (otherwise) blocks of the contraction
@@ -814,7 +808,7 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   // the sums need dpre_kernel's partial ones alone, which are complete where a product runs: they run
   // beside the last (dx, dw and dbias at m64 n1024 k1024 18.8 us, 22.4 before the products; m300
   // n2048 k2048 26.6 and 29.0)
-  if (a.dbias && runs > 1) return column_sums_launch(partial, runs, a.N, a.dbias, s, a.dx || a.dw);
+  if (a.dbias && runs > 1) return column_sums_launch(partial, runs, a.N, a.dbias, s, a.dx || a.dw ? kBeside : kAfter);
   return cudaSuccess;
 }
 

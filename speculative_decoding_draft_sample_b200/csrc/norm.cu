@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
   const RowFeed<3> feed = {ring, full,
                            {static_cast<const char*>(a.s), static_cast<const char*>(a.dy), static_cast<const char*>(a.dsum)},
                            stages, a.H * es, a.M};
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the column sums, which wait for this kernel
   feed.start();
   constexpr bool kKeep = NV * N <= 16;  // weights in registers (else read again, out of L2)
   float dw[NV][N];
@@ -381,6 +382,7 @@ template <int DT, int NV>
 __global__ void __launch_bounds__(32 * kRowWarps) norm_grad_rows_kernel(NormGradArgs a) {
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
   __shared__ float sums[kRowWarps][NV * 32 * N];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the column sums, which wait for this kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = a.H / N;
   float dw[NV][N];
   uint4 wr[NV];
@@ -438,11 +440,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) norm_grad_rows_kernel(NormGrad
 // out[h] = sum over the G partial rows: 32 columns a CTA, a warp every 32nd row,
 // four of them in flight (a warp every eighth row one at a time took 7 us for 296
 // rows of 4096, more than twice as long).
-__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int G, int H, float* out, bool beside) {
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int G, int H, float* out, int order) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   float acc = 0.f;
+  if (order == kAfter) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (h < H) {
     for (int g = row; g < G; g += 128) {
       float d[4];
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
   const float t = warp_sum(part[lane][row]);
   if (lane == 0 && blockIdx.x * 32 + row < H) out[blockIdx.x * 32 + row] = t;
   // what follows in the stream may rely on the launch before being complete too
-  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (order == kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // How a call's rows are cut: threads of a block and vectors per thread (the fewest
@@ -523,7 +526,7 @@ cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
     auto kern = nvec <= 32 ? norm_grad_rows_kernel<DT, 1> : nvec <= 64 ? norm_grad_rows_kernel<DT, 2> : norm_grad_rows_kernel<DT, 4>;
     kern<<<c.blocks, 32 * kRowWarps, 0, s>>>(b);
     e = cudaGetLastError();
-    if (e == cudaSuccess && a.dweight && c.blocks > 1) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
+    if (e == cudaSuccess && a.dweight && c.blocks > 1) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s, kAfter);
     return e;
   }
   // (dweight may be aligned to 4 bytes only, the wide kernels store 16 at a time)
@@ -538,13 +541,13 @@ cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
       else
         e = cudaErrorInvalidValue;
   }
-  if (e == cudaSuccess && a.dweight && b.partial != a.dweight) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s);
+  if (e == cudaSuccess && a.dweight && b.partial != a.dweight) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s, kAfter);
   return e;
 }
 
 }  // namespace
 
-cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, bool beside) {
+cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, int order) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((H + 31) / 32);
   cfg.blockDim = dim3(1024);
@@ -553,8 +556,8 @@ cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, c
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, column_sums_kernel, partial, G, H, out, beside);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, column_sums_kernel, partial, G, H, out, order);
 }
 
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {

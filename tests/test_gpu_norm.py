@@ -182,3 +182,45 @@ def test_same_result_every_time_and_captured(cuda_ok):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dx, first) and torch.equal(dw, firstw)
+
+
+@pytest.mark.parametrize("M,H", [(5, 1024), (300, 272), (700, 4096)])
+def test_launches_in_a_row_see_each_other(cuda_ok, M, H):
+    """A launch may start before the one before it has ended: every call here reads what the
+    call before wrote, in eager mode and replayed, and a copy follows the last."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(M, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    ws = workspace(M, H)
+    a, b, dx, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(M, device="cuda")
+    dw, out = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+
+    def chain(sync=lambda: None):
+        a.copy_(x)
+        for _ in range(3):
+            sync()
+            bn.residual_norm(a, None, w, 1e-6, b, ws, rstd=rstd)
+            sync()
+            bn.residual_norm(b, x, w, 1e-6, a, ws, sum=b, rstd=rstd)
+            sync()
+        bn.residual_norm_grad(b, w, rstd, a, dx, ws, dsum=b, dweight=dw)
+        sync()
+        out.copy_(dw)
+        sync()
+        bn.residual_norm_grad(b, w, rstd, dx, dx, ws, dweight=dw)
+        sync()
+        out.add_(dw)
+
+    chain(torch.cuda.synchronize)
+    want = [t.clone() for t in (a, b, dx, rstd, dw, out)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+        chain()
+    for run in (chain, graph.replay, chain, graph.replay):
+        for t in (a, b, dx, rstd, dw, out):
+            t.fill_(7)
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip((a, b, dx, rstd, dw, out), want))
+    assert bn.read_status(ws) == (0, -1)
