@@ -33,6 +33,7 @@
 // m2048 n5120 k4096 143 us.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
 #include "host.cuh"
+#include "launch.cuh"
 #include "linear.cuh"
 #include "norm.cuh"
 #include "tcgen05.cuh"
@@ -82,7 +83,7 @@ struct Gemm {
   void* out;                // [T, F]
   void* pre;                // [T, F] or null
   int out_type, act;
-  int order;                // kAlone, or against the launch before in the stream: kBeside, kAfter
+  Order order;
   Status* status;
 };
 
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm g) {
   extern __shared__ __align__(1024) unsigned char smem[];
   if (su32(smem) & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment (the same offset in every CTA)
+    grid_wait();
     if (threadIdx.x == 0) report(g.status, DSPARK_STATUS_INTERNAL, 0);
     return;
   }
@@ -256,10 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (g.order == kAfter) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // a launch made to run beside this one may start on the SMs that it leaves free (not
-  // before the wait above: it relies on the same results)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (g.order == kAfter) grid_wait();
+  grid_release();  // behind the wait: a launch beside this one relies on the same results
 
   // The producer's and the issuer's loop have to keep up with a block of 512
   // tensor-core cycles: they run in a whole converged warp, of which one lane
@@ -572,8 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   cluster_sync();  // neither CTA leaves while the other's arrivals or loads may still reach it
   fence_after();
-  // what follows in the stream may rely on the launch before being complete too
-  if (g.order == kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g.order == kBeside) grid_wait();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -587,7 +586,8 @@ template <int ACT>
 __global__ void __launch_bounds__(256) dpre_kernel(const void* dy, const void* pre, int M, int N, int rows_per, void* dpre,
                                                    float* partial) {
   __shared__ float part[kDpreRows][256 + 8];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that waits for this kernel sets itself up
+  grid_release();
+  grid_wait();
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int n0 = blockIdx.x * 256 + lane * 8;
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows_per);
@@ -711,21 +711,7 @@ cudaError_t gemm_launch(Gemm g, const Plan& p, const CUtensorMap& ma, const CUte
   if (e == cudaSuccess && p.parts > 4)  // clusters of 16 are past the portable size
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.clusters * 2 * p.parts));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * p.parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = g.order == kAlone ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
+  return launch_early(kern, dim3((unsigned)(p.clusters * 2 * p.parts)), kThreads, kSmem, 2 * p.parts, s, ma, mb, g);
 }
 
 }  // namespace
@@ -776,8 +762,8 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
                 : a.act == DSPARK_ACT_SILU ? dpre_kernel<DSPARK_ACT_SILU>
                 : a.act == DSPARK_ACT_GELU ? dpre_kernel<DSPARK_ACT_GELU>
                                            : dpre_kernel<DSPARK_ACT_NONE>;
-    kern<<<dim3((a.N + 255) / 256, runs), 256, 0, s>>>(a.dy, a.pre, a.M, a.N, rows_per, dpre_buf, a.dbias ? partial : nullptr);
-    e = cudaGetLastError();
+    e = launch_early(kern, dim3((a.N + 255) / 256, runs), 256, 0, 1, s, a.dy, a.pre, a.M, a.N, rows_per, dpre_buf,
+                     a.dbias ? partial : nullptr);
     if (e != cudaSuccess) return e;
   }
   CUtensorMap ma, mb;
@@ -786,7 +772,6 @@ cudaError_t linear_grad_launch(const LinearGradArgs& a, cudaStream_t s) {
   g.out_type = DSPARK_BF16;
   g.act = DSPARK_ACT_NONE;
   g.status = a.status;
-  if (a.act != DSPARK_ACT_NONE || a.dbias) g.order = kAfter;
   if (a.dx) {  // lanes k, columns m, contraction n
     if (!make_map(&ma, a.w, 2, a.K, a.N, 64) || !make_map(&mb, dpre, 2, a.N, a.M, px.nt / 2)) return cudaErrorInvalidValue;
     g.T = a.M;

@@ -29,13 +29,14 @@
 // by these keys, which are unique, so neither ties nor the order of the list's
 // atomics change a result.
 //
-// Measured: b256 j6 v129280 with 42 % of the rows padded away and 5 alternatives 59 us
-// (3.9 TB/s; 54 without alternatives, 49 with neither exponentials nor alternatives);
-// b64 j6 v151936 in fp32 48 us (4.9 TB/s).
+// Measured: b256 j6 v129280 with 42 % of the rows padded away and 5 alternatives 56 us
+// (4.1 TB/s; 51 without alternatives, 46 with neither exponentials nor alternatives);
+// b64 j6 v151936 in fp32 without alternatives 40 us (5.8 TB/s).
 #include <climits>
 
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "logprobs.cuh"
 
 namespace dspark {
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   Shared& sh = *reinterpret_cast<Shared*>(shared_raw);
   constexpr int N = Vec16<DT>::N;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_wait();
   const long long r = blockIdx.x / C;
   const int q = blockIdx.x % C;
   const int b = (int)(r / a.J);
@@ -688,6 +690,7 @@ template <int DT, bool ENTROPY>
 __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a, int parts, int batches) {
   constexpr int N = Vec16<DT>::N, kPairs = N / 2;
   using W = Words<DT>;
+  grid_wait();
   const int nvec = a.V / N;
   const long long r = blockIdx.x / parts;
   const int part = blockIdx.x % parts, b = (int)(r / a.J);
@@ -765,21 +768,9 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int num_sms, cudaStream_t s) {
   int C = 1;
   while (C < kMaxCluster && rows * C < 2LL * num_sms && nvec / (2 * C) >= kThreads) C *= 2;
   auto kern = a.dtype == DSPARK_F32 ? logprobs_kernel<DSPARK_F32> : logprobs_kernel<DSPARK_BF16>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kThreads + 32);
-  cfg.dynamicSmemBytes = sizeof(Shared);
-  cfg.stream = s;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, C);
+  return launch_early(kern, dim3((unsigned)(rows * C)), kThreads + 32, (int)sizeof(Shared), C, s, a, C);
 }
 
 cudaError_t logprobs_grad_launch(const LogprobGradArgs& a, int num_sms, cudaStream_t s) {
@@ -794,8 +785,7 @@ cudaError_t logprobs_grad_launch(const LogprobGradArgs& a, int num_sms, cudaStre
   auto kern = f32 ? (ent ? logprobs_grad_kernel<DSPARK_F32, true> : logprobs_grad_kernel<DSPARK_F32, false>)
                   : (ent ? logprobs_grad_kernel<DSPARK_BF16, true> : logprobs_grad_kernel<DSPARK_BF16, false>);
   if (rows * parts > INT_MAX) return cudaErrorInvalidValue;
-  kern<<<(unsigned)(rows * parts), kThreads, 0, s>>>(a, parts, batches);
-  return cudaGetLastError();
+  return launch_early(kern, dim3((unsigned)(rows * parts)), kThreads, 0, 1, s, a, parts, batches);
 }
 
 }  // namespace dspark

@@ -189,6 +189,9 @@ struct RowFeed {
       for (int i = 0; i < stages; ++i)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(full + i)) : "memory");
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    grid_wait();
+    if (threadIdx.x == 0) {
       for (int i = 0; i < stages; ++i) issue(i);
     }
     __syncthreads();
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) norm_grad_kernel(NormGra
   const RowFeed<3> feed = {ring, full,
                            {static_cast<const char*>(a.s), static_cast<const char*>(a.dy), static_cast<const char*>(a.dsum)},
                            stages, a.H * es, a.M};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the column sums, which wait for this kernel
+  grid_release();
   feed.start();
   constexpr bool kKeep = NV * N <= 16;  // weights in registers (else read again, out of L2)
   float dw[NV][N];
@@ -343,6 +346,7 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 
 template <int DT, bool E4M3, int NV>
 __global__ void __launch_bounds__(32 * kRowWarps) norm_rows_kernel(NormArgs a) {
+  grid_wait();
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
   const int lane = threadIdx.x & 31, nvec = a.H / N;
   for (long long r = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); r < a.M; r += (long long)gridDim.x * kRowWarps) {
@@ -382,7 +386,8 @@ template <int DT, int NV>
 __global__ void __launch_bounds__(32 * kRowWarps) norm_grad_rows_kernel(NormGradArgs a) {
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
   __shared__ float sums[kRowWarps][NV * 32 * N];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the column sums, which wait for this kernel
+  grid_release();
+  grid_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = a.H / N;
   float dw[NV][N];
   uint4 wr[NV];
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   float acc = 0.f;
-  if (order == kAfter) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (order == kAfter) grid_wait();
   if (h < H) {
     for (int g = row; g < G; g += 128) {
       float d[4];
@@ -458,8 +463,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
   __syncthreads();
   const float t = warp_sum(part[lane][row]);
   if (lane == 0 && blockIdx.x * 32 + row < H) out[blockIdx.x * 32 + row] = t;
-  // what follows in the stream may rely on the launch before being complete too
-  if (order == kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (order == kBeside) grid_wait();
 }
 
 // How a call's rows are cut: threads of a block and vectors per thread (the fewest
@@ -487,8 +491,7 @@ template <typename Kern, typename Args>
 cudaError_t launch(Kern kern, const Args& a, const Cut& c, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
   if (e != cudaSuccess) return e;
-  kern<<<c.blocks, c.threads, c.smem, s>>>(a, c.stages);
-  return cudaGetLastError();
+  return launch_early(kern, c.blocks, c.threads, c.smem, 1, s, a, c.stages);
 }
 
 // Rows of up to 128 vectors: enough CTAs of 8 rows for eight on every SM.
@@ -499,8 +502,7 @@ cudaError_t norm_pick(const NormArgs& a, cudaStream_t s) {
   const int nvec = a.H / Vec16<DT>::N;
   if (nvec <= 128) {
     auto kern = nvec <= 32 ? norm_rows_kernel<DT, E4M3, 1> : nvec <= 64 ? norm_rows_kernel<DT, E4M3, 2> : norm_rows_kernel<DT, E4M3, 4>;
-    kern<<<row_blocks(a.M, 8 * 148), 32 * kRowWarps, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(kern, row_blocks(a.M, 8 * 148), 32 * kRowWarps, 0, 1, s, a);
   }
   const Cut c = make_cut(a.M, a.H, DT, 2, 2);
   switch (c.nv) {
@@ -524,8 +526,7 @@ cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
     c.blocks = row_blocks(a.M, kNormGradBlocks);
     if (c.blocks == 1) b.partial = a.dweight;  // one CTA's sums are the result
     auto kern = nvec <= 32 ? norm_grad_rows_kernel<DT, 1> : nvec <= 64 ? norm_grad_rows_kernel<DT, 2> : norm_grad_rows_kernel<DT, 4>;
-    kern<<<c.blocks, 32 * kRowWarps, 0, s>>>(b);
-    e = cudaGetLastError();
+    e = launch_early(kern, c.blocks, 32 * kRowWarps, 0, 1, s, b);
     if (e == cudaSuccess && a.dweight && c.blocks > 1) e = column_sums_launch(a.partial, c.blocks, a.H, a.dweight, s, kAfter);
     return e;
   }
@@ -547,17 +548,8 @@ cudaError_t norm_grad_pick(const NormGradArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, int order) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((H + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, column_sums_kernel, partial, G, H, out, order);
+cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, Order order) {
+  return launch_early(column_sums_kernel, dim3((H + 31) / 32), 1024, 0, 1, s, partial, G, H, out, (int)order);
 }
 
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {

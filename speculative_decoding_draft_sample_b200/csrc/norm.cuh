@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace dspark {
 
@@ -38,14 +39,7 @@ constexpr int kNormGradBlocks = 296;
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s);
 cudaError_t norm_grad_launch(const NormGradArgs& a, cudaStream_t s);
 
-// A launch that may start while the one before it in the stream still runs: kBeside
-// shares no output with it and no input that either writes, and waits for it before it
-// ends; kAfter reads what it wrote, and waits for it before its
-// first load of that.
-enum : int { kAlone, kBeside, kAfter };
-
-// out[h] = sum over g < G of partial[g, h], in a fixed order; order is kBeside or kAfter
-// (m8192 h4096 with the launch before: 52.4 us kAfter, 55.5 as a plain launch).
-cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, int order);
+// out[h] = sum over g < G of partial[g, h], in a fixed order.
+cudaError_t column_sums_launch(const float* partial, int G, int H, float* out, cudaStream_t s, Order order);
 
 }  // namespace dspark
