@@ -360,3 +360,78 @@ def test_buffers_made_by_a_call_belong_to_its_stream(cuda_ok):
     assert torch.equal(rnd.target, plain.target) and torch.equal(rnd.base, plain.base)
     assert torch.equal(got.logp, want.logp) and torch.equal(rnd.out, plain.out)
     assert got.status() == (bn.STATUS_BAD_TEMP, 1)
+
+
+def test_captured_between_streams_and_other_nodes(cuda_ok):
+    """Launches that may start early, where the node before them is a copy, a fill, another
+    stream's kernel or nothing: each still sees all that it waits for."""
+    V, M = 4096, 48
+    norm_w, w, g = parts(V, seed=11)
+    head, scores = LogitHead(norm_w, w, M), TokenScores(M, 1, V, 3)
+    src = [hidden(g, M) for _ in range(2)]
+    tok = torch.randint(0, V, (M, 1), generator=g, device="cuda", dtype=torch.int32)
+    x, delta, dx = (torch.empty_like(src[0]) for _ in range(3))
+    logits, dlogits = (torch.empty(M, V, device="cuda", dtype=BF16) for _ in range(2))
+    gl, late = torch.empty(M, 1, device="cuda"), torch.empty(M, V, device="cuda", dtype=BF16)
+    dnorm = torch.empty(H, device="cuda")
+    dw, db = torch.empty_like(w), torch.empty(V, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(sync=lambda: None):
+        main = torch.cuda.current_stream()
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record(main)
+        side.wait_event(fork)
+        with torch.cuda.stream(side):
+            delta.copy_(src[1])
+            for _ in range(4):
+                delta.mul_(1)
+            join.record(side)
+        sync()
+        x.copy_(src[0])
+        main.wait_event(join)  # a copy and another stream's kernel before the first launch
+        sync()
+        head.run(x, logits, delta=delta)
+        sync()
+        fork.record(main)
+        side.wait_event(fork)  # a launch whose stream holds nothing but another's end
+        scores.run(logits.view(M, 1, V), tok, None, stream=side)
+        with torch.cuda.stream(side):
+            gl.copy_(scores.logp)
+            join.record(side)
+        sync()
+        main.wait_event(join)
+        scores.gradient(logits.view(M, 1, V), tok, None, gl, dlogits.view(M, 1, V))
+        sync()
+        head.gradient(dlogits, dx, dweight=dw, dbias=db, dnorm_weight=dnorm)
+        sync()
+        fork.record(main)
+        side.wait_event(fork)
+        with torch.cuda.stream(side):
+            late.copy_(dlogits)
+            late.add_(dw.sum(1) + db)
+            join.record(side)
+        main.wait_event(join)
+        sync()
+
+    outs = (logits, scores.logp, scores.top_idx, dlogits, dx, dnorm, dw, db, late)
+    step(torch.cuda.synchronize)
+    want = [t.clone() for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        step()
+    first = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):  # the graph's first node
+        head.run(x, logits, delta=delta)
+    for run in (step, graph.replay, graph.replay, step):
+        for t in outs + (x, delta, gl):
+            t.fill_(3)
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    for _ in range(3):
+        logits.fill_(3)
+        first.replay()
+        assert torch.equal(logits, want[0])
+    assert head.status() == (0, -1) and scores.status() == (0, -1)
