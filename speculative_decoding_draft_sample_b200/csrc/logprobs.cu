@@ -13,10 +13,12 @@
 // maxima and the clamp below on packed bf16 pairs, differences, products and sums
 // on packed fp32 pairs, one 2^z. z = l cs - round(M cs) is one fused product (cs =
 // log2(e) / temp); the rounding of M cs is known and taken out of the thread's sums
-// at the end. Logits are clamped at M - 200 / cs, rounded down: 2^z is zero there,
-// and masked entries (-inf or the type's lowest value) add 0 * finite, never
-// 0 * inf. Rows whose maximum is itself of the size of the type's lowest value take
-// a plain second pass.
+// at the end. It is at most 1/4 there: a thread whose own maximum has |M cs| >= 2^23
+// (a column of masked entries, of whatever value) adds nothing, and where the row's
+// maximum has |M cs| >= 2^22, so that such a thread might count, a plain second pass
+// takes differences before it scales them. Logits are clamped at M - 200 / cs,
+// rounded down: 2^z is zero there, and masked entries (-inf or any finite value) add
+// 0 * finite, never 0 * inf.
 //
 // Alternatives: a thread reads a fixed column of the row's 16-byte vectors and
 // knows its column's largest entry. The n largest entries of the slice all lie
@@ -64,7 +66,8 @@ constexpr int kUnits = 256;      // list of segments to read again; where it is 
 constexpr int kSlack = 8;        // columns that the bisection may take beyond n
 constexpr float kFloorZ = -150.f;
 constexpr float kClampZ = 200.f;
-constexpr float kPlainMax = 1.0e37f;  // past this maximum (or its z) the plain pass
+constexpr float kFarZ = 8388608.f;    // 2^23: a thread's maximum past this z adds nothing (rounding of z below: 1/4)
+constexpr float kPlainZ = 4194304.f;  // 2^22: a row's maximum past this z takes the plain pass
 constexpr float kMaxTemp = 1.0e30f;   // past this a temperature is an error
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -391,7 +394,7 @@ __device__ __forceinline__ void slice_top(Shared& sh, const char* row, int v0, i
 }
 
 // s and t of a whole row whose maximum m is known, entry by entry in the plain
-// form (rows whose maximum is of the size of the type's lowest value).
+// form (rows whose maximum's z would be rounded too far).
 template <int DT>
 __device__ void plain_sums(Shared& sh, const char* row, int nvec, float cs, RowStat& c) {
   constexpr int N = Vec16<DT>::N;
@@ -529,9 +532,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
       }
     }
     if (bm > st.m) {
-      // a maximum of the size of the type's lowest value adds nothing here: another
-      // column's is larger, or the row takes the plain pass
-      const bool fits = fabsf(bm) * cs < kPlainMax;
+      // a maximum whose z is too large to round adds nothing here: another column's is
+      // larger by 2^22 or more, or the row takes the plain pass
+      const bool fits = fabsf(bm) * cs < kFarZ;
       const float bz = fits ? bm * cs : 0.f, d = fmaxf(scaled ? mz - bz : kFloorZ, kFloorZ), f = ex2(d);
       const f32x2 d2 = pack2(d, d), f2 = pack2(f, f);
 #pragma unroll
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) logprobs_kernel(Log
   RowStat c = sh.cta_stat[0];
   for (int w = 1; w < C; ++w) c = stat_merge(c, sh.cta_stat[w], cs);
   const bool bad = c.chk != c.chk || c.m == INFINITY || c.m == -INFINITY || sh.dead;
-  if (!bad && !(fabsf(c.m) < kPlainMax && fabsf(c.m) * cs < kPlainMax)) plain_sums<DT>(sh, row, nvec, cs, c);
+  if (!bad && !(fabsf(c.m) * cs < kPlainZ)) plain_sums<DT>(sh, row, nvec, cs, c);
   const float ln_s = logf(c.s);
   if (tid == 0) {
     if (bad && !sh.dead) report(a.status, DSPARK_STATUS_BAD_ROW, b);
