@@ -432,7 +432,9 @@ int dspark_token_logprobs(const void* logits, const int32_t* tok, const float* t
  * rounded once to dtype. lse and entropy are dspark_token_logprobs' outputs for
  * the same logits and temperatures (entropy is read only with g_entropy). Padded
  * rows, and rows in error (as above; here a row whose lse is not finite counts
- * as one, the logits are not looked at), get zeros. dlogits may be logits.
+ * as one, the logits are not looked at: also where max x passes fp32's range),
+ * get zeros. dlogits may be logits. Where |lse| is 4096 or more its rounding would
+ * show in p: such a row's maximum and sum are formed again (three readings).
  *
  *   logits [B, J, V] dtype, tok [B, J] i32, temp [B] f32 or NULL
  *   lse, g_logp [B, J] f32; entropy, g_entropy [B, J] f32 or both NULL

@@ -394,7 +394,8 @@ __device__ __forceinline__ void slice_top(Shared& sh, const char* row, int v0, i
 }
 
 // s and t of a whole row whose maximum m is known, entry by entry in the plain
-// form (rows whose maximum's z would be rounded too far).
+// form (rows whose maximum's z would be rounded too far; b256 j5 v129280 at
+// temperature 1e-6 125 us, 62 at 1).
 template <int DT>
 __device__ void plain_sums(Shared& sh, const char* row, int nvec, float cs, RowStat& c) {
   constexpr int N = Vec16<DT>::N;
@@ -689,8 +690,63 @@ constexpr int kGradVecs = 4;                              // vectors of a thread
 constexpr int kGradBatch = kThreads * kGradVecs;
 constexpr int kGradBatches = 2;                           // batches of a part, at most (8: 109 us, 2: 102 us at b256 j5 v129280)
 
+// lse carries p = exp(l / temp - lse) with an error of 2^-24 |lse|, and 1 / temp one of
+// the same size: 2^-11 at this bound, a quarter of a bf16 rounding. Past it (temperatures
+// below about 0.01, logits far from zero) one CTA takes the row, so that dlogits may still
+// be logits, and forms the maximum and the sum again (b256 j5 v129280 504 us, 99 below the
+// bound; b1 j5 126 us and 10.5).
+constexpr float kFarLse = 4096.f;
+constexpr float kFarInv = 1.0e30f;  // 1 / temp past this would overflow in the products
+
+template <int DT>
+__device__ __noinline__ void grad_far_row(const char* row, char* out, int nvec, Status* status, int b, int tok, float temp, float gl,
+                                          float gh, float H) {
+  constexpr int N = Vec16<DT>::N;
+  __shared__ float red[2][kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float m = -INFINITY, s = 0.f;
+  for (int i = tid; i < nvec; i += kThreads) {
+    float v[N];
+    Vec16<DT>::load(row + (size_t)i * 16, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) m = max_nan(m, v[e]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) m = max_nan(m, red[0][w]);
+  const bool bad = !(fabsf(m) < INFINITY);  // not the logits that lse was made of
+  if (bad && tid == 0) report(status, DSPARK_STATUS_BAD_ROW, b);
+  const float cs = fminf(kLog2e / temp, 3.0e38f);
+  for (int i = tid; i < nvec; i += kThreads) {
+    float v[N];
+    Vec16<DT>::load(row + (size_t)i * 16, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) s += ex2(zdiff(v[e], m, cs));
+  }
+  s = warp_sum(s);
+  if (lane == 0) red[1][warp] = s;
+  __syncthreads();  // every entry has been read twice: the output may take the logits' place
+  s = 0.f;
+  for (int w = 0; w < kThreads / 32; ++w) s += red[1][w];
+  const float ln_s = logf(s);
+  for (int i = tid; i < nvec; i += kThreads) {
+    float v[N];
+    Vec16<DT>::load(row + (size_t)i * 16, v);
+    alignas(16) typename Elem<DT>::T o[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float lp = fmaxf((v[e] - m) / temp, -200.f) - ln_s, p = ex2(lp * kLog2e);
+      const float d = ((i * N + e == tok ? gl : 0.f) - p * fmaf(gh, lp + H, gl)) / temp;
+      o[e] = Elem<DT>::store_round(bad ? 0.f : d);
+    }
+    *reinterpret_cast<uint4*>(out + (size_t)i * 16) = *reinterpret_cast<const uint4*>(o);
+  }
+}
+
 template <int DT, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a, int parts, int batches) {
+__global__ void __launch_bounds__(kThreads, 5) logprobs_grad_kernel(LogprobGradArgs a, int parts, int batches) {
   constexpr int N = Vec16<DT>::N, kPairs = N / 2;
   using W = Words<DT>;
   grid_wait();
@@ -712,7 +768,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
     for (int i = i0; i < i1; i += kThreads) *reinterpret_cast<uint4*>(out + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const float inv = 1.f / (tau > 0.f ? tau : 1.f);
+  const float temp = tau > 0.f ? tau : 1.f, inv = 1.f / temp;
+  if (!(fabsf(lse) < kFarLse && inv < kFarInv)) {
+    if (part == 0) grad_far_row<DT>(row, out, nvec, a.status, b, tok, temp, gl, gh, H);
+    return;
+  }
   const float c1 = -gh * inv, c0 = fmaf(c1, H, -gl * inv);
   const f32x2 inv2 = pack2(inv, inv), lse2 = pack2(-lse, -lse), e2 = pack2(kLog2e, kLog2e);
   const f32x2 c02 = pack2(c0, c0), c12 = pack2(c1, c1);
