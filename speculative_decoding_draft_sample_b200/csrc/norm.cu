@@ -466,6 +466,9 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial,
   if (order == kBeside) grid_wait();
 }
 
+// Shared memory that the rings of an SM's blocks have together.
+constexpr int kRing = 216 * 1024;
+
 // How a call's rows are cut: threads of a block and vectors per thread (the fewest
 // of 1, 2, 4, 8 that 512 threads cover a row with), blocks per SM, and the ring's
 // depth (up to 4 rows within the SM's shared memory).
@@ -478,7 +481,6 @@ inline Cut make_cut(int M, int H, int dtype, int arrays, int most_blocks) {
   c.nv = 1;
   while (c.nv < 8 && nvec > c.nv * 512) c.nv *= 2;
   c.threads = ((nvec + c.nv - 1) / c.nv + 31) / 32 * 32;
-  constexpr int kRing = 216 * 1024;
   int per_sm = c.nv > most_blocks ? 1 : (c.threads > 256 ? 2 : 4);
   while (per_sm > 1 && kRing / per_sm < 2 * row) per_sm /= 2;
   c.stages = max(1, min(kMaxStages, kRing / per_sm / row));
@@ -487,9 +489,12 @@ inline Cut make_cut(int M, int H, int dtype, int arrays, int most_blocks) {
   return c;
 }
 
+// The kernel's limit is the largest ring of any call, the same in every call: it belongs
+// to the kernel on its device, and a call of another host thread may set it between this
+// call's setting and its launch.
 template <typename Kern, typename Args>
 cudaError_t launch(Kern kern, const Args& a, const Cut& c, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
   if (e != cudaSuccess) return e;
   return launch_early(kern, c.blocks, c.threads, c.smem, 1, s, a, c.stages);
 }
