@@ -521,11 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_residual(after);
       }
       const int f0 = w.tf * kTileF + rank * kLanes, t0 = w.tt * g.nt;
+      // scales and bias through L2 (__ldcg): the launch before, beside which this one may have
+      // started, may have written them, and the read-only path's cache need not show that
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int f = f0 + row0 + 8 * i;
-        ls[i] = g.lane_scale && f < g.F ? __ldg(g.lane_scale + f) : 0.f;
-        bias[i] = g.bias && f < g.F ? __ldg(g.bias + f) : 0.f;
+        ls[i] = g.lane_scale && f < g.F ? __ldcg(g.lane_scale + f) : 0.f;
+        bias[i] = g.bias && f < g.F ? __ldcg(g.bias + f) : 0.f;
       }
       const int c1 = min(g.nt, g.T - t0);
       Residual next = {};
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t src = tmem + buf * kMaxCols + ((uint32_t)(quarter * 32) << 16);
       for (int c = group * kCols; c < c1; c += kStep) {
         float v[kCols];
-        const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldg(g.col_scale + t0 + c + lane) : 0.f;
+        const float cscale = g.col_scale && t0 + c + lane < g.T ? __ldcg(g.col_scale + t0 + c + lane) : 0.f;
         if constexpr (STAGED)
           tmem_ld_frags(src + c, v);
         else
