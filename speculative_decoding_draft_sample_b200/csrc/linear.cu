@@ -92,10 +92,11 @@ __device__ __forceinline__ float gate(float z, float v) { return __fdividef(z, 1
 
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-// act'(z); past |z| = 64 both gates are 0 or 1 exactly
+// act'(z). At |z| = 128 the gates are 0 or 1 exactly (2^184 is infinite in fp32), and
+// so they stay for larger |z|, whose cubes and products would overflow
 __device__ __forceinline__ float activate_grad(float z, int act) {
   if (act == DSPARK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-  z = z != z ? z : fminf(fmaxf(z, -64.f), 64.f);
+  z = z != z ? z : fminf(fmaxf(z, -128.f), 128.f);
   const float v = act == DSPARK_ACT_SILU ? z : kGelu2 * fmaf(0.044715f * z * z, z, z);
   const float dv = act == DSPARK_ACT_SILU ? 1.f : kGelu2 * fmaf(3.f * 0.044715f * z, z, 1.f);
   const float g = __fdividef(1.f, 1.f + ex2(-v * kLog2e));
