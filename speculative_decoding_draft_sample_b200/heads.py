@@ -67,6 +67,8 @@ class LogitHead:
         self.y = torch.empty((rows, H), dtype=weight.dtype, device=dev)
         self.y_scale = torch.empty((rows,), **f32) if self.e4m3 else None
         self.rstd = torch.empty((rows,), **f32)
+        self._ran = 0  # rows of the run whose y, sum and rstd the buffers hold
+        self._captured = False  # a run is in a graph: which one was the last, its replays decide
 
     def run(self, hidden: torch.Tensor, logits: torch.Tensor, delta: Optional[torch.Tensor] = None, stream=None) -> None:
         """hidden, delta [..., H] bfloat16 -> logits [..., V] (bfloat16 or float32); the summed
@@ -78,16 +80,21 @@ class LogitHead:
                                  f"{self.rows} rows, H={self.H}, V={self.V}")
         d = delta.reshape(-1, self.H) if delta is not None and delta.is_contiguous() else delta
         y, y_scale = self.y[:M], self.y_scale[:M] if self.e4m3 else None
+        self._ran = 0
+        self._captured = self._captured or (x.is_cuda and torch.cuda.is_current_stream_capturing())
         bn.residual_norm(x, d, self.norm_weight, self.eps, y, self.ws, sum=self.sum[:M], y_scale=y_scale,
                          rstd=self.rstd[:M], stream=stream)
         out = logits.view(M, self.V) if logits.is_contiguous() else logits
         bn.linear(y, self.weight, out, self.ws, x_scale=y_scale, w_scale=self.w_scale, bias=self.bias,
                   stream=stream)
+        self._ran = M
 
     def gradient(self, dlogits: torch.Tensor, dhidden: torch.Tensor, dweight: Optional[torch.Tensor] = None,
                  dbias: Optional[torch.Tensor] = None, dnorm_weight: Optional[torch.Tensor] = None, stream=None) -> None:
-        """The gradients of the last ``run`` of this many rows: dlogits [..., V] bfloat16 -> dhidden
-        [..., H] (hidden's and delta's alike), and where given dweight [V, H], dbias [V] and
+        """The gradients of the last ``run``, whose rows these must be (a run of another batch in
+        between replaces what they are made of; after a captured run, whose replays are not seen
+        here, that is the caller's to keep): dlogits [..., V] bfloat16 -> dhidden [..., H]
+        (hidden's and delta's alike), and where given dweight [V, H], dbias [V] and
         dnorm_weight [H] f32. Frozen weights are left out and cost nothing."""
         if self.e4m3:
             raise bn.DSparkError("an 8-bit head has no gradient")
@@ -95,6 +102,8 @@ class LogitHead:
         M = dl.shape[0]
         if not 1 <= M <= self.rows or dhidden.numel() != M * self.H:
             raise bn.DSparkError(f"dlogits {tuple(dlogits.shape)} and dhidden {tuple(dhidden.shape)} do not fit the head")
+        if M != self._ran and not self._captured:
+            raise bn.DSparkError(f"gradient of {M} rows after a run of {self._ran}")
         dx = dhidden.view(M, self.H) if dhidden.is_contiguous() else dhidden
         # dx holds the gradient of the norm's output between the two calls
         bn.linear_grad(self.y[:M], self.weight, dl, self.ws, dx=dx, dw=dweight, dbias=dbias, stream=stream)

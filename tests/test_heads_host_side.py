@@ -1,0 +1,59 @@
+"""What the heads and the round decide on the host, on CPU tensors with the device calls replaced
+by recorders."""
+import pytest
+import torch
+
+from speculative_decoding_draft_sample_b200 import binding as bn
+from speculative_decoding_draft_sample_b200 import build, heads
+
+V, H, ROWS = 64, 32, 12
+BF16 = torch.bfloat16
+
+
+@pytest.fixture()
+def calls(monkeypatch):
+    build.build()
+    made = []
+    for name in ("residual_norm", "linear", "linear_grad", "residual_norm_grad", "token_logprobs"):
+        monkeypatch.setattr(bn, name, lambda *a, _n=name, **k: made.append((_n, a, k)))
+    return made
+
+
+def head():
+    return heads.LogitHead(torch.ones(H, dtype=BF16), torch.zeros(V, H, dtype=BF16), ROWS)
+
+
+def bf(*shape):
+    return torch.zeros(*shape, dtype=BF16)
+
+
+def test_gradient_needs_the_run_it_belongs_to(calls):
+    h = head()
+    with pytest.raises(bn.DSparkError, match="after a run of 0"):
+        h.gradient(bf(4, V), bf(4, H))
+    h.run(bf(4, H), bf(4, V))
+    for rows in (3, 5, ROWS):               # rows that the run did not write, or other rows
+        with pytest.raises(bn.DSparkError, match="after a run of 4"):
+            h.gradient(bf(rows, V), bf(rows, H))
+    assert [c[0] for c in calls] == ["residual_norm", "linear"]
+    h.gradient(bf(4, V), bf(4, H))
+    h.gradient(bf(2, 2, V), bf(2, 2, H))    # again, and in another shape of as many rows
+    h.run(bf(ROWS, H), bf(ROWS, V))
+    with pytest.raises(bn.DSparkError, match="after a run of 12"):
+        h.gradient(bf(4, V), bf(4, H))
+    h.gradient(bf(ROWS, V), bf(ROWS, H))
+    assert [c[0] for c in calls].count("linear_grad") == 3
+
+
+def test_a_run_that_failed_leaves_nothing_to_derive(calls, monkeypatch):
+    h = head()
+    h.run(bf(4, H), bf(4, V))
+
+    def refuse(*a, **k):
+        raise bn.DSparkError("refused")
+
+    monkeypatch.setattr(bn, "linear", refuse)
+    with pytest.raises(bn.DSparkError, match="refused"):
+        h.run(bf(4, H), bf(4, V))
+    with pytest.raises(bn.DSparkError, match="after a run of 0"):
+        h.gradient(bf(4, V), bf(4, H))
