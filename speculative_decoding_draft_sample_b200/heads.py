@@ -33,6 +33,11 @@ def quantize_rows(w: torch.Tensor, chunk: int = 8192) -> Tuple[torch.Tensor, tor
     return q, scale
 
 
+def _width(t: torch.Tensor) -> int:
+    """Entries of a row: the last dimension, which a head never spreads over rows."""
+    return t.shape[-1] if t.dim() else -1
+
+
 class LogitHead:
     """logits = norm(hidden + delta) @ weight^T (+ bias) for up to ``rows`` rows.
 
@@ -73,10 +78,12 @@ class LogitHead:
     def run(self, hidden: torch.Tensor, logits: torch.Tensor, delta: Optional[torch.Tensor] = None, stream=None) -> None:
         """hidden, delta [..., H] bfloat16 -> logits [..., V] (bfloat16 or float32); the summed
         residual stream stays in ``sum``."""
-        x = hidden.reshape(-1, self.H) if hidden.is_contiguous() else hidden
+        rows_fit = _width(hidden) == self.H and _width(logits) == self.V and (delta is None or _width(delta) == self.H)
+        x = hidden.reshape(-1, self.H) if rows_fit and hidden.is_contiguous() else hidden
         M = x.shape[0] if x.dim() == 2 else -1
-        if not 1 <= M <= self.rows or logits.numel() != M * self.V:
-            raise bn.DSparkError(f"hidden {tuple(hidden.shape)} and logits {tuple(logits.shape)} do not fit a head of "
+        if not rows_fit or not 1 <= M <= self.rows or logits.numel() != M * self.V:
+            shapes = f"hidden {tuple(hidden.shape)}" + (f", delta {tuple(delta.shape)}" if delta is not None else "")
+            raise bn.DSparkError(f"{shapes} and logits {tuple(logits.shape)} do not fit a head of "
                                  f"{self.rows} rows, H={self.H}, V={self.V}")
         d = delta.reshape(-1, self.H) if delta is not None and delta.is_contiguous() else delta
         y, y_scale = self.y[:M], self.y_scale[:M] if self.e4m3 else None
@@ -98,9 +105,10 @@ class LogitHead:
         dnorm_weight [H] f32. Frozen weights are left out and cost nothing."""
         if self.e4m3:
             raise bn.DSparkError("an 8-bit head has no gradient")
-        dl = dlogits.reshape(-1, self.V) if dlogits.is_contiguous() else dlogits
-        M = dl.shape[0]
-        if not 1 <= M <= self.rows or dhidden.numel() != M * self.H:
+        rows_fit = _width(dlogits) == self.V and _width(dhidden) == self.H
+        dl = dlogits.reshape(-1, self.V) if rows_fit and dlogits.is_contiguous() else dlogits
+        M = dl.shape[0] if dl.dim() else -1
+        if not rows_fit or not 1 <= M <= self.rows or dhidden.numel() != M * self.H:
             raise bn.DSparkError(f"dlogits {tuple(dlogits.shape)} and dhidden {tuple(dhidden.shape)} do not fit the head")
         if M != self._ran and not self._captured:
             raise bn.DSparkError(f"gradient of {M} rows after a run of {self._ran}")

@@ -24,7 +24,7 @@ def head():
 
 
 def bf(*shape):
-    return torch.zeros(*shape, dtype=BF16)
+    return torch.zeros(shape, dtype=BF16)
 
 
 def test_gradient_needs_the_run_it_belongs_to(calls):
@@ -57,3 +57,35 @@ def test_a_run_that_failed_leaves_nothing_to_derive(calls, monkeypatch):
         h.run(bf(4, H), bf(4, V))
     with pytest.raises(bn.DSparkError, match="after a run of 0"):
         h.gradient(bf(4, V), bf(4, H))
+
+
+@pytest.mark.parametrize("hidden,logits,delta", [
+    ((2, 2 * H), (4, V), None),              # as many values as four rows of H
+    ((4, H), (V, 4), None),
+    ((4, H), (2, 2 * V), None),
+    ((4, H), (4, V), (2, 2 * H)),
+    ((4 * H,), (4, V), None),
+    ((3, H + 1), (3, V), None),
+    ((), (), None),
+])
+def test_rows_of_another_width_are_refused(calls, hidden, logits, delta):
+    with pytest.raises(bn.DSparkError, match="do not fit"):
+        head().run(bf(*hidden), bf(*logits), delta=None if delta is None else bf(*delta))
+    assert calls == []
+
+
+@pytest.mark.parametrize("dlogits,dhidden", [((2, 2 * V), (4, H)), ((4, V), (H, 4)), ((V, 4), (4, H)), ((4, V + 1), (4, H)), ((), ())])
+def test_gradients_of_another_width_are_refused(calls, dlogits, dhidden):
+    h = head()
+    h.run(bf(4, H), bf(4, V))
+    with pytest.raises(bn.DSparkError, match="do not fit"):
+        h.gradient(bf(*dlogits), bf(*dhidden))
+    assert len(calls) == 2
+
+
+def test_rows_may_be_shaped_otherwise_on_either_side(calls):
+    h = head()
+    h.run(bf(2, 2, H), bf(4, V), delta=bf(4, 1, H))
+    h.run(bf(4, H), bf(2, 2, V))
+    h.gradient(bf(2, 2, V), bf(4, H))
+    assert [c[0] for c in calls] == ["residual_norm", "linear"] * 2 + ["linear_grad", "residual_norm_grad"]
