@@ -110,7 +110,8 @@ class SpecRound:
         # logits made from hidden states, when a round is given heads
         self.target = self.base = None
         self.verified = None  # the target logits of the last run
-        self.scores: Optional[TokenScores] = None
+        self.scores: Optional[TokenScores] = None  # of the last score()
+        self._scores: Dict[int, TokenScores] = {}  # by n_top: a captured score() goes on writing to its own
         self.cut = torch.empty((B,), **i32)
         self.survival = torch.empty((B, K), **f32)
         self.accepted = torch.empty((B,), **i32)
@@ -216,12 +217,13 @@ class SpecRound:
         verified with, at temperatures ``temp`` [B] (the round's, or None for 1): their log
         probabilities, entropies and n_top alternatives, zeros and -1 behind the emitted
         tokens. Row j of a request holds its j-th emitted token. The scores stay in buffers
-        of this round that the next call overwrites."""
+        of this round that the next call with as many alternatives overwrites."""
         if self.verified is None:
             raise bn.DSparkError("score() needs a run() before it")
-        if self.scores is None or (0 if self.scores.top_idx is None else self.scores.top_idx.shape[2]) != n_top:
+        if n_top not in self._scores:
             with torch.cuda.stream(stream):  # the workspace is cleared in order with the call
-                self.scores = TokenScores(self.B, self.K + 1, self.V, n_top, self.dtype, self.x.device)
+                self._scores[n_top] = TokenScores(self.B, self.K + 1, self.V, n_top, self.dtype, self.x.device)
+        self.scores = self._scores[n_top]
         self.scores.run(self.verified, self.out, temp, stream=stream)
         return self.scores
 

@@ -89,3 +89,19 @@ def test_rows_may_be_shaped_otherwise_on_either_side(calls):
     h.run(bf(4, H), bf(2, 2, V))
     h.gradient(bf(2, 2, V), bf(4, H))
     assert [c[0] for c in calls] == ["residual_norm", "linear"] * 2 + ["linear_grad", "residual_norm_grad"]
+
+
+def test_scores_keep_their_buffers_between_counts_of_alternatives(calls):
+    """A graph may still write the buffers of an earlier call with another n_top."""
+    from speculative_decoding_draft_sample_b200.spec_round import SpecRound
+    rnd = SpecRound(2, 3, V, 64, device="cpu")
+    rnd.verified = bf(2, 4, V)
+    five, none = rnd.score(None, n_top=5), rnd.score(None)
+    places = [t.data_ptr() for t in (five.logp, five.top_idx, five.ws)]
+    del five
+    taken = {none.logp.data_ptr(), none.ws.data_ptr()} | {torch.zeros_like(none.ws).data_ptr() for _ in range(8)}
+    again = rnd.score(None, n_top=5)
+    assert [t.data_ptr() for t in (again.logp, again.top_idx, again.ws)] == places
+    assert not taken & set(places)
+    assert rnd.scores is again and rnd.score(None) is none
+    assert [c[1][3].data_ptr() for c in calls] == [again.logp.data_ptr(), none.logp.data_ptr()] * 2
