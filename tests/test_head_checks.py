@@ -215,3 +215,31 @@ def test_workspace_sizes(lib):
     # backward: dpre (with an activation) and column sums of up to ceil(M / 32) runs of rows
     assert bn.workspace_bytes(bn.OP_LINEAR, 40, 2, 256, 16, bn.BF16) == 256 + 2 * 256 * 4
     assert bn.workspace_bytes(bn.OP_LINEAR, 40, 1, 256, 16, bn.BF16) == 256 + 40 * 256 * 2 + 2 * 256 * 4
+
+
+BIG = 2 ** 32 + 8   # rows that a C int would carry as 8
+
+
+def test_sizes_past_a_c_int_are_refused():
+    def meta(*shape, dtype=bf):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    ws = meta(1 << 16, dtype=torch.uint8)
+    for call in (
+            lambda: bn.residual_norm(meta(BIG, 8), None, meta(8), 1e-6, meta(BIG, 8), ws),
+            lambda: bn.residual_norm_grad(meta(BIG, 8), meta(8), meta(BIG, dtype=f32), meta(BIG, 8), meta(BIG, 8), ws),
+            lambda: bn.linear(meta(BIG, 8), meta(8, 8), meta(BIG, 8), ws),
+            lambda: bn.linear(meta(8, 8), meta(BIG, 8), meta(8, BIG), ws),
+            lambda: bn.linear(meta(8, BIG), meta(8, BIG), meta(8, 8), ws),
+            lambda: bn.linear_grad(meta(BIG, 8), meta(8, 8), meta(BIG, 8), ws, dw=meta(8, 8)),
+            lambda: bn.token_logprobs(meta(BIG, 1, 8), meta(BIG, 1, dtype=i32), None, meta(BIG, 1, dtype=f32), ws),
+            lambda: bn.token_logprobs(meta(1, 1, BIG), meta(1, 1, dtype=i32), None, meta(1, 1, dtype=f32), ws),
+            lambda: bn.token_logprobs(meta(1, 1, 16), meta(1, 1, dtype=i32), None, meta(1, 1, dtype=f32), ws,
+                                      top_idx=meta(1, 1, BIG, dtype=i32), top_logp=meta(1, 1, BIG, dtype=f32)),
+            lambda: bn.token_logprobs_grad(meta(BIG, 1, 8), meta(BIG, 1, dtype=i32), None, meta(BIG, 1, dtype=f32),
+                                           meta(BIG, 1, dtype=f32), meta(BIG, 1, 8), ws)):
+        with pytest.raises(bn.DSparkError, match="2\\*\\*31"):
+            call()
+    for sizes in ((BIG, 1, 8, 0), (1, BIG, 8, 0), (1, 1, BIG, 0)):
+        assert bn.workspace_bytes(bn.OP_LOGPROBS, *sizes, bn.BF16) == 0
+    assert bn.workspace_bytes(bn.OP_LINEAR, 8, 0, 8, BIG, bn.BF16) == 0
