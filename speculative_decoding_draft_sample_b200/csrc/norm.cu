@@ -500,7 +500,7 @@ cudaError_t launch(Kern kern, const Args& a, const Cut& c, cudaStream_t s) {
 }
 
 // Rows of up to 128 vectors: enough CTAs of 8 rows for eight on every SM.
-inline int row_blocks(int M, int most) { return min((M + kRowWarps - 1) / kRowWarps, most); }
+inline int row_blocks(int M, int most) { return min((M - 1) / kRowWarps + 1, most); }  // (M may be INT_MAX)
 
 template <int DT, bool E4M3>
 cudaError_t norm_pick(const NormArgs& a, cudaStream_t s) {
