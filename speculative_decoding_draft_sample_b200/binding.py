@@ -176,10 +176,9 @@ def _call(name: str, device: torch.device, args, stream) -> None:
 _INT_MAX = 2 ** 31 - 1
 
 
-def _sizes(*sizes: int) -> None:
+def _too_large(*sizes: int) -> None:
     """The library takes sizes as C ints; ctypes would hand on the low 32 bits of a larger one."""
-    if max(sizes) > _INT_MAX:
-        raise DSparkError(f"a call's sizes must be below 2**31, got {sizes}")
+    raise DSparkError(f"a call's sizes must be below 2**31, got {sizes}")
 
 
 def workspace_bytes(op: int, B: int, K: int, V: int, r: int, dtype: int) -> int:
@@ -393,7 +392,8 @@ def token_logprobs(logits, tok, temp, logp, ws, entropy=None, lse=None, top_idx=
         if top_idx.dim() != 3:
             raise DSparkError(f"top_idx must have shape {(B, J)} + (n,), got {tuple(top_idx.shape)}")
         n = top_idx.shape[2]
-    _sizes(B, J, V, n)
+    if B > _INT_MAX or J > _INT_MAX or V > _INT_MAX or n > _INT_MAX:
+        _too_large(B, J, V, n)
     args = (
         _ptr(logits, "logits", None, (B, J, V), dev), _ptr(tok, "tok", i32, (B, J), dev),
         _ptr(temp, "temp", f32, (B,), dev), B, J, V, _dtype_code(logits), n,
@@ -410,7 +410,8 @@ def token_logprobs_grad(logits, tok, temp, lse, g_logp, dlogits, ws, entropy=Non
     (entropy and g_entropy go together) with respect to the logits -> dlogits
     (which may be logits)."""
     B, J, V = logits.shape
-    _sizes(B, J, V)
+    if B > _INT_MAX or J > _INT_MAX or V > _INT_MAX:
+        _too_large(B, J, V)
     dev, f32 = logits.device, torch.float32
     if (entropy is None) != (g_entropy is None):
         raise DSparkError("entropy and g_entropy go together")
@@ -430,7 +431,8 @@ def residual_norm(x, delta, weight, eps: float, y, ws, sum=None, y_scale=None, r
     float8_e4m3fn with y_scale [M]), and where given sum [M,H] (x + delta; it may be x or
     delta) and rstd [M]."""
     M, H = x.shape
-    _sizes(M, H)
+    if M > _INT_MAX or H > _INT_MAX:
+        _too_large(M, H)
     dev, f32 = x.device, torch.float32
     e4m3 = y.dtype == torch.float8_e4m3fn
     if e4m3 != (y_scale is not None):
@@ -449,7 +451,8 @@ def residual_norm_grad(s, weight, rstd, dy, dx, ws, dsum=None, dweight=None, str
     """dspark_residual_norm_grad: s [M,H] (the stored sum), rstd [M], dy [M,H], dsum [M,H] or None
     -> dx [M,H] (which may be dy or dsum), and where given dweight [H] f32."""
     M, H = s.shape
-    _sizes(M, H)
+    if M > _INT_MAX or H > _INT_MAX:
+        _too_large(M, H)
     dev, f32 = s.device, torch.float32
     args = (
         _ptr(s, "s", None, (M, H), dev), _ptr(weight, "weight", s.dtype, (H,), dev),
@@ -473,7 +476,8 @@ def linear(x, w, y, ws, x_scale=None, w_scale=None, bias=None, residual=None, pr
     (float32 or bfloat16), residual (which may be y) and pre share a dtype."""
     M, K = x.shape
     N = w.shape[0]
-    _sizes(M, N, K)
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large(M, N, K)
     dev, f32 = x.device, torch.float32
     e4m3 = x.dtype == torch.float8_e4m3fn
     if not e4m3 and x.dtype != torch.bfloat16:
@@ -496,7 +500,8 @@ def linear_grad(x, w, dy, ws, dx=None, dw=None, dbias=None, pre=None, act: str =
     dx [M,K], dw [N,K] and dbias [N] f32."""
     M, K = x.shape
     N = w.shape[0]
-    _sizes(M, N, K)
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large(M, N, K)
     dev, bf16 = x.device, torch.bfloat16
     args = (
         _ptr(x, "x", bf16, (M, K), dev), _ptr(w, "w", bf16, (N, K), dev),
