@@ -11,7 +11,7 @@
 // next launch's CTAs start on SMs that come free; without it they start at the kernel's
 // end. A kernel that a kBeside launch follows, which relies on all that the kernel itself
 // relies on, releases after its own grid_wait. The products release (m1536 n129280 k4096
-// e4m3 573 us, 584 without), so do kernels that a launch of the same call follows; norm
+// e4m3 573 us in short runs, 584 without), so do kernels that a launch of the same call follows; norm
 // and log probabilities do not (16.5 and 44 us, 16.2 and 40 without, for m1536 h7168 and
 // b64 j6 v151936 fp32: early CTAs of the next call leave this one's rows uneven).
 #pragma once

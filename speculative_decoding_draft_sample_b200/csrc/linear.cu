@@ -28,9 +28,11 @@
 // the contraction; the other pairs leave their fp32 sums in the first one's shared
 // memory (its ring is free by then), which adds them in the order of the parts and
 // finishes the tile.
-// Measured (short runs): m1536 n129280 k4096 1090 us in bf16 (1.49 PFLOP/s), 549 us in
-// e4m3 (2.96 PFLOP/s); m16 n129280 k4096 165 us (6.4 TB/s, memory bounds it); gradient
-// m2048 n5120 k4096 143 us.
+// Measured in steady repeats, under the power cap (in brackets: ten calls from a cool
+// chip): m1536 n129280 k4096 1222 us in bf16 (1063; 1.33 PFLOP/s), 667 us in e4m3 (581;
+// 2.44 PFLOP/s); m16 n129280 k4096 164 us (6.5 TB/s, memory bounds it); gradient
+// m2048 n5120 k4096 with gelu 159 us (137). The other figures of this file come from
+// short runs of both sides in turn.
 // Every wait is bounded; a CTA that gives up reports DSPARK_STATUS_TIMEOUT.
 #include "host.cuh"
 #include "launch.cuh"
@@ -87,7 +89,8 @@ struct Gemm {
   Status* status;
 };
 
-// z / (1 + exp(-v)): silu with v = z, gelu's tanh form with v = 2 sqrt(2/pi) (z + 0.044715 z^3)
+// z / (1 + exp(-v)) by a power of two and the fast division (together 2^-21 of the result
+// and 2^-23 |v|; also where the output is fp32): silu with v = z, gelu's tanh form with v = 2 sqrt(2/pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float gate(float z, float v) { return __fdividef(z, 1.f + ex2(-v * kLog2e)); }
 
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -653,7 +656,10 @@ struct Plan {
 // in ns: a block of the contraction by its width (74 pairs, m1024 n18944, k2048
 // against k1024; up to 64 columns the issuing loop bounds it); a tile at least its
 // epilogue; the first loads and the last epilogue are not hidden; a joined tile has
-// two cluster barriers and the parts' sums on top. Clusters of 2, 4, 8 and 16 CTAs
+// two cluster barriers and the parts' sums on top. The epilogue's cost is that of a plain
+// staged one: a residual, pre, an activation or odd rows are not in it, and where the
+// contraction is short they bound the tile (m1536 n64000 k512 with a residual takes 132 us
+// where this says 79). Clusters of 2, 4, 8 and 16 CTAs
 // of this size run 74, 33, 15 and 7 at once.
 Plan make_plan(long long F, long long T, int kblocks, bool b_cols) {
   constexpr int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};

@@ -106,7 +106,9 @@ __device__ __forceinline__ float2 row_factors(const NormArgs& a, long long r, fl
   return make_float2(rstd, inv);
 }
 
-// Vector i of row r: the sum and y.
+// Vector i of row r: the sum and y. e4m3: v w times rstd and 1 / scale, two rounded fp32
+// factors where the definition divides once; 2^-23 of the value, so an entry next to a tie
+// of e4m3 may fall on its other side.
 template <int DT, bool E4M3>
 __device__ __forceinline__ void write_row(const NormArgs& a, long long r, int i, const float* v, const uint4& wr, float2 k) {
   constexpr int N = Vec16<DT>::N, es = Elem<DT>::kBytes;
