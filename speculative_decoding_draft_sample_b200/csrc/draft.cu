@@ -180,7 +180,8 @@ static cudaError_t launch_simt(const DraftArgs& a, int k, cudaStream_t s) {
   const size_t sm = (size_t)BT * a.r * sizeof(float);
   if (sm > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(draft_logits_simt<DT, BT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         BT * 1024 * (int)sizeof(float));  // r <= 1024, alike in every call
     if (e != cudaSuccess) return e;
   }
   draft_logits_simt<DT, BT><<<grid, 256, sm, s>>>(a, k);

@@ -228,8 +228,11 @@ cudaError_t prefix_schedule_launch(const SchedArgs& a, cudaStream_t s) {
     return cudaGetLastError();
   }
   const size_t sm = prefix_schedule_smem(a.B, a.K);
+  // the largest size of any call (K = 1), whatever this call's: the limit belongs to the
+  // kernel, and another host thread may set it before the launch below
+  constexpr int kMost = kMaxScheduleItems * (int)(sizeof(uint64_t) + sizeof(int));
   cudaError_t e = cudaFuncSetAttribute(prefix_schedule_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;
   prefix_schedule_kernel<<<1, kSchedThreads, sm, s>>>(a);
   return cudaGetLastError();

@@ -22,6 +22,8 @@ typedef int (*norm_fn)(const void*, const void*, const void*, int, int, int, flo
                        void*, size_t, void*);
 typedef int (*grad_fn)(const void*, const void*, const float*, const void*, const void*, int, int, int, void*, float*,
                        void*, size_t, void*);
+typedef int (*sched_fn)(const float*, const float*, const float*, float, int, int, int, float, int*, float*, void*, size_t,
+                        void*);
 struct job {
   void* fn;
   int gradient, M, H, dtype, times, rc, failed;
@@ -42,10 +44,22 @@ static void* loop(void* p) {
   }
   return NULL;
 }
+static void* schedules(void* p) {  /* x: confidence logits, weight: position temperatures, rstd: step costs, y: cut, dx: survival */
+  struct job* j = (struct job*)p;
+  for (int i = 0; i < j->times; ++i) {
+    int rc = ((sched_fn)j->fn)((float*)j->x, (float*)j->weight, (float*)j->rstd, 1.0f, j->M, j->H, 0, 0.0f, (int*)j->y,
+                               (float*)j->dx, j->ws, j->bytes, j->stream);
+    if (rc != 0) {
+      j->rc = rc;
+      ++j->failed;
+    }
+  }
+  return NULL;
+}
 int run_at_once(struct job* jobs, int n) {
   pthread_t t[8];
   for (int i = 0; i < n; ++i)
-    if (pthread_create(&t[i], NULL, loop, &jobs[i])) return -1;
+    if (pthread_create(&t[i], NULL, jobs[i].gradient == 2 ? schedules : loop, &jobs[i])) return -1;
   for (int i = 0; i < n; ++i) pthread_join(t[i], NULL);
   return 0;
 }
@@ -96,3 +110,25 @@ def test_norms_of_two_widths(cuda_ok, runner, dtype, widths, gradient):
     assert [(j.failed, j.rc) for j in jobs] == [(0, 0), (0, 0)]
     for k in kept:
         assert torch.equal(k[3], k[7]) and torch.equal(k[4], k[8])
+
+
+def test_schedules_of_two_sizes(cuda_ok, runner):
+    jobs, kept = (Job * 2)(), []
+    for job, (B, K) in zip(jobs, [(64, 8), (1024, 8)]):
+        conf, pos_temp = torch.randn(B, K, device="cuda"), torch.ones(K, device="cuda")
+        cost = torch.arange(B * (K + 1), device="cuda", dtype=torch.float32) * 0.01
+        cut, survival = torch.empty(B, device="cuda", dtype=torch.int32), torch.empty(B, K, device="cuda")
+        ws = torch.zeros(bn.workspace_bytes(bn.OP_SCHEDULE, B, K, 8, 1, bn.F32), dtype=torch.uint8, device="cuda")
+        bn.prefix_schedule(conf, pos_temp, cost, 1.0, bn.CUT_COST, 0.0, cut, survival, ws)
+        stream = torch.cuda.Stream()
+        kept.append((conf, pos_temp, cost, ws, stream, cut, survival, cut.clone(), survival.clone()))
+        job.fn = ctypes.cast(bn.lib().dspark_prefix_schedule, ctypes.c_void_p).value
+        job.gradient, job.M, job.H, job.times = 2, B, K, 5000
+        job.x, job.weight, job.rstd, job.y, job.dx = (t.data_ptr() for t in (conf, pos_temp, cost, cut, survival))
+        job.ws, job.stream, job.bytes = ws.data_ptr(), stream.cuda_stream, ws.numel()
+    torch.cuda.synchronize()
+    assert runner(jobs, 2) == 0
+    torch.cuda.synchronize()
+    assert [(j.failed, j.rc) for j in jobs] == [(0, 0), (0, 0)]
+    for k in kept:
+        assert torch.equal(k[5], k[7]) and torch.equal(k[6], k[8])
