@@ -417,7 +417,8 @@ int dspark_sts_fit(const float* conf_logit, const uint8_t* survived, int N, int 
  *   logp [B, J] f32 out; entropy, lse [B, J] f32 out or NULL
  *   top_idx [B, J, n_top] i32 out, top_logp [B, J, n_top] f32 out (NULL with n_top 0)
  * Limits: 1 <= B <= 65535, 1 <= J <= 64, 8 <= V < 2^24, V % 8 == 0,
- * 0 <= n_top <= min(32, V). Each row is read once; sums are fp32.
+ * 0 <= n_top <= min(32, V). Each row is read once (twice where |max x| passes 2.9e6);
+ * sums are fp32.
  * Workspace: dspark_workspace_bytes(DSPARK_OP_LOGPROBS, B, J, V, 0, dtype) (the
  * status block alone). One launch.
  */
